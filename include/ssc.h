@@ -412,6 +412,133 @@ int ssc_sparse_conv3d_bwd(const void* plan, int64_t n_in, int64_t n_out, int32_t
                           const void* dout, void* dfeats, void* dweight, void* dbias, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norm of queries and keys with position rotation, for attention over voxel
+ * rows.  For every row i and head h of the queries and of the keys, x = the
+ * head's head_dim elements, and
+ *   u = x * w / sqrt(mean(x^2) + eps)                   (norm != 0; else u = x)
+ *   pair j = (u_a, u_b) turns by 2 pi * turns[j] * positions[i][axis[j]]:
+ *   y_a = u_a cos - u_b sin,  y_b = u_a sin + u_b cos.
+ * Pairs are (2j, 2j + 1) or (j, j + pairs); the head_dim - 2 * pairs
+ * dimensions past them are not turned.  Backward, with g = dy turned back and
+ * r = 1 / sqrt(mean(x^2) + eps):
+ *   dw = sum over rows of g x r,  dx = r (g w - x r mean(g w x r)).
+ * A position is any int32; its turns are reduced in 64 bits.  Sums are fp32
+ * and outputs are rounded once; weight gradients are summed in a fixed order.
+ * ------------------------------------------------------------------------ */
+#define SSC_MAX_ATTN_ROWS (1LL << 28)
+#define SSC_MAX_ROPE_AXES 8
+
+enum ssc_rope_layout {
+  SSC_ROPE_INTERLEAVED = 0,  /* pair j = elements 2j and 2j + 1 */
+  SSC_ROPE_HALVES = 1        /* pair j = elements j and j + pairs */
+};
+
+/* Sizes of a call (a host struct, read during the call).  Strides are in
+ * elements, multiples of 16 bytes, not negative; a head's elements are
+ * contiguous, so the heads may be views of one packed projection. */
+typedef struct ssc_norm_rope_shape {
+  int64_t n;                             /* rows, at most SSC_MAX_ATTN_ROWS */
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  int64_t pos_row_stride;                /* int32s from one row of positions to the next */
+  int32_t heads_q, heads_kv;             /* either may be 0 (its pointers unused); at most 1024 */
+  int32_t head_dim;                      /* whole 16-byte vectors, at most 256 */
+  int32_t dtype;
+  int32_t axes;                          /* columns of positions, at most SSC_MAX_ROPE_AXES */
+  int32_t pairs;                         /* turned pairs; 0: no rotation */
+  int32_t layout;                        /* ssc_rope_layout; HALVES: pairs fill whole 16-byte vectors */
+  int32_t norm;                          /* 0: rotation only (weights NULL) */
+  int32_t weight_per_head;               /* weights are [heads][head_dim], else [head_dim] for all heads */
+  float eps;
+} ssc_norm_rope_shape;
+
+/*
+ * q [n][heads_q][head_dim], k [n][heads_kv][head_dim] (strided), positions
+ * [n][axes] int32 (4-byte aligned), turns [pairs] double: revolutions per unit
+ * of position, axis [pairs] int32: each pair's column of positions (taken into
+ * [0, axes)), weights `dtype` or NULL (ones).  q_out, k_out contiguous, out;
+ * they may not overlap the inputs.
+ */
+int ssc_qk_norm_rope_fwd(const ssc_norm_rope_shape* shape, const void* q, const void* k,
+                         const int32_t* positions, const double* turns, const int32_t* axis,
+                         const void* q_weight, const void* k_weight, void* q_out, void* k_out, void* stream);
+
+/* Workspace bytes of ssc_qk_norm_rope_bwd; 0 for invalid or unsupported
+ * arguments.  Needs no GPU. */
+size_t ssc_qk_norm_rope_workspace_bytes(const ssc_norm_rope_shape* shape);
+
+/*
+ * Backward pass: dq_out, dk_out contiguous output gradients; dq, dk
+ * contiguous, out; dq_weight, dk_weight of the weights' shapes, out.  Each
+ * output may be NULL to skip it.  The workspace is read only when a weight
+ * gradient is asked for.
+ */
+int ssc_qk_norm_rope_bwd(const ssc_norm_rope_shape* shape, const void* q, const void* k,
+                         const int32_t* positions, const double* turns, const int32_t* axis,
+                         const void* q_weight, const void* k_weight, const void* dq_out, const void* dk_out,
+                         void* dq, void* dk, void* dq_weight, void* dk_weight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Cross attention of ragged samples: the rows of sample b, q_offsets[b] ..
+ * q_offsets[b + 1] - 1, attend that sample's key rows, kv_offsets[b] ..
+ * kv_offsets[b + 1] - 1 (an encoder's states, or the voxels' own rows for self
+ * attention).  Per query head h, with key head h / (heads_q / heads_kv) and
+ * over the keys j whose kv_mask byte is not zero:
+ *   s_j = scale * q . k_j,  m = max s_j,  l = sum exp(s_j - m),
+ *   out = sum exp(s_j - m) v_j / l,  lse = m + ln l;
+ * backward, with P_j = exp(s_j - lse):
+ *   dv_j = sum P_j dout,  dS_j = P_j (dout . v_j - dout . out),
+ *   dq = scale sum dS_j k_j,  dk_j = scale sum dS_j q,
+ * sums over rows including all query heads of a shared key head.  A row with
+ * no key (an empty sample, every key masked, or every score -inf) gives zeros,
+ * lse = -inf and no gradient; a masked key's row is never used, whatever it
+ * holds, and its gradient is zero.  Rows before the first or from the last
+ * offset belong to no sample: as queries they have no key, as keys no query.
+ * Offsets must not decrease; they are taken into [0, rows].
+ * Scores, statistics and sums are fp32.  Probabilities (and dS) are rounded to
+ * `dtype` for the second products; in fp16 they carry a power of two that
+ * keeps small ones normal.  Sums run in a fixed order: results repeat.
+ * ------------------------------------------------------------------------ */
+#define SSC_MAX_HEAD_DIM 128
+#define SSC_MAX_ATTN_BATCH 65536
+
+/* Sizes of a call (a host struct, read during the call).  Strides as in
+ * ssc_norm_rope_shape; 0 is allowed (a broadcast input). */
+typedef struct ssc_attn_shape {
+  int64_t nq, nk;                        /* rows, each at most SSC_MAX_ATTN_ROWS; nq * heads_q / heads_kv <= 2^30 */
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int32_t batch;                         /* samples, 1 .. SSC_MAX_ATTN_BATCH */
+  int32_t heads_q, heads_kv;             /* heads_q a multiple of heads_kv, at most 1024 */
+  int32_t head_dim;                      /* whole 16-byte vectors, at most SSC_MAX_HEAD_DIM */
+  int32_t dtype;
+  float scale;                           /* finite */
+} ssc_attn_shape;
+
+/* Workspace bytes of ssc_cross_attn_fwd (backward 0) or _bwd (backward 1); 0
+ * for invalid or unsupported arguments.  Needs no GPU. */
+size_t ssc_cross_attn_workspace_bytes(const ssc_attn_shape* shape, int32_t backward);
+
+/*
+ * q [nq][heads_q][head_dim], k and v [nk][heads_kv][head_dim] (strided),
+ * offsets [batch + 1] int32 in device memory, kv_mask [nk] bytes or NULL (all
+ * attended).  out [nq][heads_q][head_dim] contiguous, lse [heads_q][nq] fp32,
+ * both out.
+ */
+int ssc_cross_attn_fwd(const ssc_attn_shape* shape, const void* q, const void* k, const void* v,
+                       const int32_t* q_offsets, const int32_t* kv_offsets, const uint8_t* kv_mask, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward pass: out and lse as the forward pass wrote them, dout contiguous
+ * as out; dq, dk, dv contiguous, out, each NULL to skip it. */
+int ssc_cross_attn_bwd(const ssc_attn_shape* shape, const void* q, const void* k, const void* v,
+                       const void* out, const float* lse, const void* dout, const int32_t* q_offsets,
+                       const int32_t* kv_offsets, const uint8_t* kv_mask, void* dq, void* dk, void* dv,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code (host only). */
 const char* ssc_status_string(int status);
 

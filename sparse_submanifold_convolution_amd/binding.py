@@ -57,6 +57,12 @@ SIGNATURES = {
                                              _SZ, _VP]),
     "ssc_sparse_conv3d_bwd": (ctypes.c_int, [_VP, _I64, _I64, _I32, _VP, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP,
                                              _VP, _VP, _SZ, _VP]),
+    "ssc_qk_norm_rope_fwd": (ctypes.c_int, [_VP] * 11),
+    "ssc_qk_norm_rope_workspace_bytes": (_SZ, [_VP]),
+    "ssc_qk_norm_rope_bwd": (ctypes.c_int, [_VP] * 15 + [_SZ, _VP]),
+    "ssc_cross_attn_workspace_bytes": (_SZ, [_VP, _I32]),
+    "ssc_cross_attn_fwd": (ctypes.c_int, [_VP] * 10 + [_SZ, _VP]),
+    "ssc_cross_attn_bwd": (ctypes.c_int, [_VP] * 14 + [_SZ, _VP]),
 }
 
 SEQ_MODES = {"z_order": 0, "hilbert": 1}
