@@ -504,8 +504,12 @@ int ssc_qk_norm_rope_bwd(const ssc_norm_rope_shape* shape, const void* q, const 
 #define SSC_MAX_HEAD_DIM 128
 #define SSC_MAX_ATTN_BATCH 65536
 
+/* a tile's 64 rows are addressed with 32-bit byte offsets from its first */
+#define SSC_MAX_ATTN_ROW_STRIDE (1LL << 23)
+
 /* Sizes of a call (a host struct, read during the call).  Strides as in
- * ssc_norm_rope_shape; 0 is allowed (a broadcast input). */
+ * ssc_norm_rope_shape, row strides at most SSC_MAX_ATTN_ROW_STRIDE elements; 0
+ * is allowed (a broadcast input). */
 typedef struct ssc_attn_shape {
   int64_t nq, nk;                        /* rows, each at most SSC_MAX_ATTN_ROWS; nq * heads_q / heads_kv <= 2^30 */
   int64_t q_row_stride, q_head_stride;

@@ -11,9 +11,23 @@ import math
 
 import torch
 
-from .binding import DTYPE_CODE, SSCError, _check, _need, _ptr, _stream, lib
+from .binding import DTYPE_CODE, SSCError, _check, _need, lib
 
 ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(device: torch.device) -> int:
+    # the handle itself: a Stream object costs more than a small call's kernel
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _new(like: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of like's shape and type."""
+    return torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
 
 
 class _NormRopeShape(ctypes.Structure):
@@ -135,9 +149,9 @@ def qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None, positions: 
                      layout: str = "interleaved"):
     """ssc_qk_norm_rope_fwd: q [n, Hq, D], k [n, Hk, D] (views of a packed projection are taken as they are; either may
     be None) -> (q_out, k_out) contiguous.  positions: int32 [n, axes], for example coords[:, 1:]."""
-    sh, dev, dt, qs, ks = _rope_shape(q, k, positions, table, q_weight, k_weight, eps, norm, layout)
-    qo = torch.empty(qs, dtype=dt, device=dev) if q is not None else None
-    ko = torch.empty(ks, dtype=dt, device=dev) if k is not None else None
+    sh, dev, *_ = _rope_shape(q, k, positions, table, q_weight, k_weight, eps, norm, layout)
+    qo = _new(q) if q is not None else None
+    ko = _new(k) if k is not None else None
     _check("ssc_qk_norm_rope_fwd",
            lib().ssc_qk_norm_rope_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), *_table_ptrs(positions, table),
                                       _ptr(q_weight), _ptr(k_weight), _ptr(qo), _ptr(ko), _stream(dev)))
@@ -155,8 +169,8 @@ def qk_norm_rope_bwd(q: torch.Tensor | None, k: torch.Tensor | None, positions: 
         _need(dq_out, "dq_out", dt, qs, dev)
     if dk_out is not None:
         _need(dk_out, "dk_out", dt, ks, dev)
-    dq = torch.empty(qs, dtype=dt, device=dev) if dq_out is not None else None
-    dk = torch.empty(ks, dtype=dt, device=dev) if dk_out is not None else None
+    dq = torch.empty_like(dq_out) if dq_out is not None else None
+    dk = torch.empty_like(dk_out) if dk_out is not None else None
     dqw = torch.empty_like(q_weight) if need_weights and q_weight is not None and dq_out is not None else None
     dkw = torch.empty_like(k_weight) if need_weights and k_weight is not None and dk_out is not None else None
     ws = None
@@ -249,10 +263,10 @@ def cross_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     """ssc_cross_attn_fwd: q [nq, Hq, D] attends k, v [nk, Hk, D] sample by sample -> (out [nq, Hq, D], lse [Hq, nq]).
 
     Offsets are int32 [batch + 1] on the device, kv_mask [nk] bool (True: attended), scale 1 / sqrt(D) by default."""
-    sh, dev, dt = _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
+    sh, dev, _ = _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
     ws = _attn_workspace(sh, 0, dev)
-    out = torch.empty(q.shape, dtype=dt, device=dev)
-    lse = torch.empty((sh.heads_q, sh.nq), dtype=torch.float32, device=dev)
+    out = _new(q)
+    lse = q.new_empty((sh.heads_q, sh.nq), dtype=torch.float32)
     _check("ssc_cross_attn_fwd",
            lib().ssc_cross_attn_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(q_offsets), _ptr(kv_offsets),
                                     _ptr(kv_mask), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)))
@@ -269,9 +283,9 @@ def cross_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
     _need(dout, "dout", dt, tuple(q.shape), dev)
     _need(lse, "lse", torch.float32, (sh.heads_q, sh.nq), dev)
     ws = _attn_workspace(sh, 1, dev)
-    dq = torch.empty(q.shape, dtype=dt, device=dev) if need_dq else None
-    dk = torch.empty(k.shape, dtype=dt, device=dev) if need_dk else None
-    dv = torch.empty(v.shape, dtype=dt, device=dev) if need_dv else None
+    dq = torch.empty_like(dout) if need_dq else None
+    dk = _new(k) if need_dk else None
+    dv = _new(v) if need_dv else None
     _check("ssc_cross_attn_bwd",
            lib().ssc_cross_attn_bwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                                     _ptr(q_offsets), _ptr(kv_offsets), _ptr(kv_mask), _ptr(dq), _ptr(dk), _ptr(dv),

@@ -35,13 +35,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kTile = 64;  // streamed rows per LDS stage
+// streamed rows of an LDS tile: 32 for fp32, whose 64 would not fit the registers on their way
+constexpr int tile_rows(int esize) { return esize == 4 ? 32 : 64; }
 
 struct Params {
   const void *q, *k, *v, *out, *dout;
   void *o, *dq, *dk, *dv;
   float* lse;          // [hq][nq]
-  float* delta;        // [hq][nq], backward: sum over d of dout * out
+  float* delta;        // [hq][nq], backward: sum over d of dout * out, as the dQ pass corrects it
   const uint32_t* bound;  // backward, fp16: bits of max |dout row|^2 and max |v row|^2
   const int32_t *qoff, *koff;
   const uint8_t* mask;
@@ -52,7 +53,8 @@ struct Params {
   int32_t gshift;      // r / G = (r * gmul) >> gshift for r < 2^31
   float scale;
   int32_t tiles, nsplit;
-  float *part_a, *part_b;  // splits: partial sums [nsplit][rows][d]; forward part_b: [nsplit][rows][2] (max, sum)
+  // splits: partial sums [nsplit][rows][d]; forward part_b: [nsplit][rows][2] (max, sum); dQ part_e: [nsplit][rows]
+  float *part_a, *part_b, *part_e;
 };
 
 template <typename T>
@@ -68,6 +70,10 @@ struct Elt<float> {
     for (int j = 0; j < 4; ++j)
       c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
     return c;
+  }
+  // acc + the products of the elements two words hold
+  __device__ static __forceinline__ float dot(uint32_t a, uint32_t b, float acc) {
+    return fmaf(__uint_as_float(a), __uint_as_float(b), acc);
   }
   // fragment s of a 32x32 result: its registers 4s .. 4s+3
   __device__ static __forceinline__ u32x4 pack(const f32x16& p, int s) {
@@ -89,6 +95,9 @@ struct Elt<_Float16> {
   }
   __device__ static __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+  }
+  __device__ static __forceinline__ float dot(uint32_t a, uint32_t b, float acc) {
+    return fmaf(hi(a), hi(b), fmaf(lo(a), lo(b), acc));
   }
   __device__ static __forceinline__ u32x4 pack(const f32x16& p, int s) {
     u32x4 f;
@@ -113,6 +122,9 @@ struct Elt<__bf16> {
   }
   __device__ static __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  }
+  __device__ static __forceinline__ float dot(uint32_t a, uint32_t b, float acc) {
+    return fmaf(hi(a), hi(b), fmaf(lo(a), lo(b), acc));
   }
   __device__ static __forceinline__ u32x4 pack(const f32x16& p, int s) {
     u32x4 f;
@@ -149,12 +161,13 @@ __device__ __forceinline__ s16x4 lds_tr16(const void* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(const_cast<void*>(p)));
 }
 
-// Geometry of one LDS tile of kTile streamed rows and DP (head size rounded up to 32) elements, and its reads
+// Geometry of one LDS tile of kRows streamed rows and DP (head size rounded up to 32) elements, and its reads
 template <typename T, int DP>
 struct TileOf {
   static constexpr int kVec = Elt<T>::kVec;
   static constexpr int CPR = DP / kVec;            // chunks per row
-  static constexpr int kBytes = kTile * CPR * 16;
+  static constexpr int kRows = tile_rows(sizeof(T)), kGroups = kRows / 32;
+  static constexpr int kBytes = kRows * CPR * 16;
   static constexpr int kFrags = DP / (2 * kVec);   // operand fragments along the head dimension
   static constexpr int kBlocks = DP / 32;          // 32-wide blocks of the head dimension
 
@@ -193,25 +206,33 @@ struct TileOf {
   }
 };
 
-// A tile on its way from memory to LDS, NT threads: 16-byte chunks in registers
+// A tile on its way from memory to LDS, NT threads (a workgroup, or one wave): 16-byte chunks in registers.  The loads go through a buffer
+// descriptor that ends with the sample's last row, so rows past it (and chunks past the head) read as zeros with no
+// branch, and a thread's offsets inside a tile are computed once for all tiles.
 template <typename T, int DP, int NT>
 struct Stage {
   using TL = TileOf<T, DP>;
-  static constexpr int kTotal = kTile * TL::CPR;
+  static constexpr int kTotal = TL::kRows * TL::CPR;
   static constexpr int N = (kTotal + NT - 1) / NT;
   u32x4 r[N];
-  __device__ static __forceinline__ int item(int i) { return int(threadIdx.x) + i * NT; }
+  uint32_t off[N];
+  __device__ static __forceinline__ int item(int i) { return int(threadIdx.x) % NT + i * NT; }
   __device__ static __forceinline__ bool any(int i) { return kTotal % NT == 0 || item(i) < kTotal; }
-  // ptr(row): address of row `row` of the tile, called for rows below `rows` only; dchunks: chunks the head fills
-  template <typename F>
-  __device__ __forceinline__ void load(int rows, int dchunks, F ptr) {
+  // row_bytes: from one row to the next; dchunks: chunks the head fills
+  __device__ __forceinline__ void init(uint32_t row_bytes, int dchunks) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int row = item(i) / TL::CPR, c = item(i) % TL::CPR;
-      r[i] = u32x4{0, 0, 0, 0};
-      if (any(i) && row < rows && c < dchunks)
-        r[i] = *reinterpret_cast<const u32x4*>(ptr(row) + c * TL::kVec);
+      off[i] = (any(i) && c < dchunks) ? uint32_t(row) * row_bytes + uint32_t(c) * 16u : 0xFFFFFFF0u;
     }
+  }
+  // the tile at `base`, of whose rows `rows` (> 0) exist, each of head_bytes
+  __device__ __forceinline__ void load(const void* base, int rows, int64_t row_bytes, uint32_t head_bytes) {
+    const int64_t span = int64_t(rows - 1) * row_bytes + head_bytes;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                                        int(span < 0xFFFFFFE0ll ? uint32_t(span) : 0xFFFFFFE0u), 0x00027000);
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, int(off[i]), 0, 0));
   }
   __device__ __forceinline__ void store(char* tile) const {
 #pragma unroll
@@ -227,6 +248,12 @@ struct Stage {
       if (!keep[i]) r[i] = u32x4{0, 0, 0, 0};
   }
 };
+
+// a value every lane holds alike, in scalar registers
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return int64_t(uint64_t(uint32_t(uniform(int(v >> 32)))) << 32 | uint32_t(uniform(int(v))));
+}
 
 __device__ __forceinline__ int64_t clamp_off(const int32_t* off, int i, int64_t n) {
   const int64_t v = off[i];
@@ -263,23 +290,22 @@ __device__ __forceinline__ bool find_segment(const int32_t* off, int64_t n, cons
       const int o = __shfl_up(incl, d);
       if (lane >= d) incl += o;
     }
-    const int total = __shfl(incl, 63);
+    const int total = uniform(__shfl(incl, 63));
     if (t - before < total) {
       const uint64_t past = __ballot(incl > t - before);
-      const int w = __ffsll((unsigned long long)past) - 1;
-      const int sw = __builtin_amdgcn_readfirstlane(base + w);
-      // every lane reads the same values again: uniform, so they sit in scalar registers
+      const int w = uniform(__ffsll((unsigned long long)past) - 1);
+      const int sw = uniform(base + w);
       const int64_t bw = sw == 0 ? 0 : clamp_off(off, sw - 1, n);
       const int64_t ew = sw == batch + 1 ? n : clamp_off(off, sw, n);
-      seg->begin = bw;
-      seg->len = int(ew > bw ? ew - bw : 0);
-      seg->tile = __builtin_amdgcn_readfirstlane(t - before - __shfl(incl - mine, w));
+      seg->begin = uniform(bw);
+      seg->len = uniform(int(ew > bw ? ew - bw : 0));
+      seg->tile = uniform(t - before - __shfl(incl - mine, w));
       seg->other = 0;
       seg->other_len = 0;
       if (sw >= 1 && sw <= batch) {
         const int64_t ob = clamp_off(other_off, sw - 1, other_n), oe = clamp_off(other_off, sw, other_n);
-        seg->other = ob;
-        seg->other_len = int(oe > ob ? oe - ob : 0);
+        seg->other = uniform(ob);
+        seg->other_len = uniform(int(oe > ob ? oe - ob : 0));
       }
       return true;
     }
@@ -300,332 +326,30 @@ __device__ __forceinline__ int64_t xcd_item(int64_t items) {
 }
 inline unsigned xcd_grid(int64_t items) { return unsigned((items + 7) / 8 * 8); }
 
-// the tiles [first, last) of `len` streamed rows that split `s` of `n` takes
-__device__ __forceinline__ void split_range(int len, int s, int n, int* first, int* last) {
-  const int tiles = (len + kTile - 1) / kTile, per = (tiles + n - 1) / n;
+// the share [first, last) of `tiles` streamed tiles that split `s` of `n` takes
+__device__ __forceinline__ void split_range(int tiles, int s, int n, int* first, int* last) {
+  const int per = (tiles + n - 1) / n;
   *first = s * per < tiles ? s * per : tiles;
   *last = *first + per < tiles ? *first + per : tiles;
 }
 
+// Column blocks of 32 a wave keeps (queries forward and for dQ, keys for dK and dV), and the waves per SIMD the
+// registers are held to.
+struct Cfg {
+  int fwd_qb, fwd_occ, dq_qb, dq_occ, dkv_kb, dkv_occ;
+};
+constexpr Cfg tile_cfg(int esize, int dp) {
+  return dp <= 64 ? Cfg{1, 2, 1, 2, 1, 2} : Cfg{1, esize == 4 ? 1 : 2, 1, 1, 1, 1};
+}
+
+// keeps a wave's LDS writes before the reads that follow; the hardware serves them in order
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ float half_swap(float v) { return __shfl_xor(v, 32); }
-
-// ---------------------------------------------------------------------------
-// forward
-// ---------------------------------------------------------------------------
-
-template <typename T, int DP, int NW, int QB, bool MASK>
-__global__ void __launch_bounds__(NW * 64) fwd_kernel(Params p) {
-  using TL = TileOf<T, DP>;
-  using E = Elt<T>;
-  constexpr int NT = NW * 64, TC = NW * QB * 32;
-  __shared__ __align__(16) char lk[2][TL::kBytes];
-  __shared__ __align__(16) char lv[2][TL::kBytes];
-  __shared__ unsigned long long lvalid[2];
-  const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
-  if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
-  const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
-  Segment sg;
-  if (!find_segment(p.qoff, p.nq, p.koff, p.nk, p.batch, p.G, TC, tile, &sg)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-  const int dchunks = p.d / TL::kVec;
-  // the running maximum is taken on unscaled scores: a negative scale's sign goes into the queries (exactly), and a
-  // scale of zero clears them (a masked score's -inf times 0 would be NaN)
-  const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
-  const uint32_t clear = p.scale == 0.f ? 0u : ~0u;
-  const uint32_t flip = p.scale < 0.f ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
-
-  // this lane's query columns
-  int64_t row[QB];
-  int head[QB];
-  bool live[QB];
-  u32x4 qf[QB][TL::kFrags];
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const uint32_t r = uint32_t(sg.tile) * TC + (wave * QB + b) * 32 + (lane & 31);
-    live[b] = r < uint32_t(sg.len) * uint32_t(p.G);
-    const uint32_t rc = live[b] ? r : 0u, tok = div_g(rc, p);
-    row[b] = sg.begin + tok;
-    head[b] = hk * p.G + int(rc - tok * uint32_t(p.G));
-    const T* qp = static_cast<const T*>(p.q) + row[b] * p.q_row + head[b] * p.q_head;
-#pragma unroll
-    for (int f = 0; f < TL::kFrags; ++f) {
-      const int ch = 2 * f + half;
-      qf[b][f] = u32x4{0, 0, 0, 0};
-      if (live[b] && ch < dchunks) {
-        qf[b][f] = *reinterpret_cast<const u32x4*>(qp + ch * TL::kVec);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qf[b][f][e] = (qf[b][f][e] & clear) ^ flip;
-      }
-    }
-  }
-
-  f32x16 o[QB][TL::kBlocks];
-  float m[QB], l[QB];
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    m[b] = -INFINITY;
-    l[b] = 0.f;
-#pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) o[b][d] = f32x16{};
-  }
-
-  int t0, t1;
-  split_range(sg.other_len, split, p.nsplit, &t0, &t1);
-  const T* kp = static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head;
-  const T* vp = static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head;
-  Stage<T, DP, NT> sk, sv;
-  uint8_t keep[Stage<T, DP, NT>::N];
-  bool kept = false;  // the key of streamed row `lane`
-  auto load = [&](int t) {
-    const int64_t k0 = int64_t(t) * kTile;
-    const int rows = sg.other_len - t * kTile;
-    sk.load(rows, dchunks, [&](int r) { return kp + (k0 + r) * p.k_row; });
-    sv.load(rows, dchunks, [&](int r) { return vp + (k0 + r) * p.v_row; });
-    if constexpr (MASK) {
-      const uint8_t* mp = p.mask + sg.other + k0;
-#pragma unroll
-      for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
-        const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
-        keep[i] = (r < rows && r < kTile) ? mp[r] : 0;
-      }
-      kept = lane < rows && mp[lane] != 0;
-    }
-  };
-  if (t0 < t1) load(t0);
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    if constexpr (MASK) {
-      sk.clear(keep);
-      sv.clear(keep);
-      const uint64_t w = __ballot(kept);
-      if (threadIdx.x == 0) lvalid[buf] = w;
-    }
-    sk.store(lk[buf]);
-    sv.store(lv[buf]);
-    __syncthreads();
-    const int rows = sg.other_len - t * kTile;
-    uint64_t valid = rows >= kTile ? ~0ull : (1ull << rows) - 1;
-    if constexpr (MASK) valid = lvalid[buf];
-    if (t + 1 < t1) load(t + 1);
-    if (MASK && valid == 0) continue;
-
-    f32x16 s[QB][2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-      for (int b = 0; b < QB; ++b) s[b][kb] = f32x16{};
-#pragma unroll
-      for (int f = 0; f < TL::kFrags; ++f) {
-        const u32x4 a = TL::rows(lk[buf], 32 * kb, f);
-#pragma unroll
-        for (int b = 0; b < QB; ++b) s[b][kb] = E::mma(a, qf[b][f], s[b][kb]);
-      }
-    }
-    if (~valid != 0) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const uint32_t w = uint32_t(valid >> (32 * kb)) >> (4 * half);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool on = (w >> (8 * (r / 4) + r % 4)) & 1u;
-#pragma unroll
-          for (int b = 0; b < QB; ++b) s[b][kb][r] = on ? s[b][kb][r] : -INFINITY;
-        }
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      float mx = s[b][0][0];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][kb][r]);
-      mx = fmaxf(mx, half_swap(mx)) * c;
-      const float mn = fmaxf(m[b], mx);
-      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing attended yet
-      const float al = __builtin_amdgcn_exp2f(m[b] - ref);
-      m[b] = mn;
-      l[b] *= al;
-      const float sh = float(kPExp<T>) - ref;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[b][kb][r], c, sh));
-          s[b][kb][r] = e;
-          l[b] += e;
-        }
-#pragma unroll
-      for (int d = 0; d < TL::kBlocks; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[b][d][r] *= al;
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int st = 0; st < E::kSteps; ++st) {
-        u32x4 pf[QB];
-#pragma unroll
-        for (int b = 0; b < QB; ++b) pf[b] = E::pack(s[b][kb], st);
-#pragma unroll
-        for (int d = 0; d < TL::kBlocks; ++d) {
-          const u32x4 a = TL::cols(lv[buf], 32 * kb, st, d);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) o[b][d] = E::mma(a, pf[b], o[b][d]);
-        }
-      }
-  }
-
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const float total = l[b] + half_swap(l[b]);
-    if (!live[b]) continue;
-    const bool some = total != 0.f;  // NaN counts
-    if (p.nsplit > 1) {
-      const int64_t at = (int64_t(split) * p.nq + row[b]) * p.hq + head[b];
-      if (half == 0) {
-        p.part_b[2 * at] = m[b];
-        p.part_b[2 * at + 1] = total;
-      }
-      if (some) {
-        float* op = p.part_a + at * p.d;
-#pragma unroll
-        for (int d = 0; d < TL::kBlocks; ++d)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int e = 32 * d + 8 * g + 4 * half;
-            if (e < p.d) *reinterpret_cast<float4*>(op + e) = make_float4(o[b][d][4 * g], o[b][d][4 * g + 1], o[b][d][4 * g + 2], o[b][d][4 * g + 3]);
-          }
-      }
-      continue;
-    }
-    const float inv = some ? 1.f / total : 0.f;
-    if (half == 0) p.lse[int64_t(head[b]) * p.nq + row[b]] = some ? (m[b] - float(kPExp<T>)) * kLn2 + logf(total) : -INFINITY;
-    T* op = static_cast<T*>(p.o) + (row[b] * p.hq + head[b]) * p.d;
-#pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int e = 32 * d + 8 * g + 4 * half;
-        if (e < p.d) {
-          const float f0 = o[b][d][4 * g] * inv, f1 = o[b][d][4 * g + 1] * inv, f2 = o[b][d][4 * g + 2] * inv,
-                      f3 = o[b][d][4 * g + 3] * inv;
-          if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float4*>(op + e) = make_float4(f0, f1, f2, f3);
-          else
-            *reinterpret_cast<uint2*>(op + e) = make_uint2(E::pack2(f0, f1), E::pack2(f2, f3));
-        }
-      }
-  }
-}
-
-// Joins the splits of the forward pass: a wave per (row, head)
-template <typename T>
-__global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t rh = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6), n = p.nq * p.hq;
-  if (rh >= n) return;
-  float mx = -INFINITY;
-  for (int s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, p.part_b[2 * (s * n + rh)]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.nsplit; ++s) {
-    const float ls = p.part_b[2 * (s * n + rh) + 1];
-    if (ls == 0.f) continue;
-    const float w = __builtin_amdgcn_exp2f(p.part_b[2 * (s * n + rh)] - ref);
-    total += w * ls;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + 64 * e < p.d) acc[e] += w * p.part_a[(s * n + rh) * p.d + lane + 64 * e];
-  }
-  const bool some = total != 0.f;
-  const float inv = some ? 1.f / total : 0.f;
-  T* op = static_cast<T*>(p.o) + rh * p.d;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 64 * e < p.d) op[lane + 64 * e] = T(acc[e] * inv);
-  if (lane == 0)
-    p.lse[(rh % p.hq) * p.nq + rh / p.hq] = some ? (mx - float(kPExp<T>)) * kLn2 + logf(total) : -INFINITY;
-}
-
-// ---------------------------------------------------------------------------
-// backward
-// ---------------------------------------------------------------------------
-
-// delta[h][i] = sum over d of dout * out: a wave per four (row, head) pairs of 16 lanes.  fp16: also the largest
-// |dout row|^2 and |v row|^2 (maxima: any order gives the same), which bound dS for its scaling to fp16's range.
-template <typename T>
-__global__ void __launch_bounds__(256) delta_kernel(Params p, uint32_t* bound) {
-  constexpr int kVec = Elt<T>::kVec;
-  const int sub = threadIdx.x & 15;
-  const int64_t id = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4), nd = p.nq * p.hq;
-  const int chunks = p.d / kVec;
-  float acc = 0.f, sq = 0.f;
-  const bool isq = id < nd;
-  const int64_t vi = id - nd;
-  const bool isv = sizeof(T) == 2 && bound && !isq && vi < p.nk * p.hk && (!p.mask || p.mask[vi / p.hk]);
-  if (isq || isv) {
-    const T* a = isq ? static_cast<const T*>(p.dout) + id * p.d
-                     : static_cast<const T*>(p.v) + vi / p.hk * p.v_row + vi % p.hk * p.v_head;
-    const T* o = static_cast<const T*>(p.out) + id * p.d;
-    for (int ch = sub; ch < chunks; ch += 16) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(a + ch * kVec);
-      u32x4 y = u32x4{0, 0, 0, 0};
-      if (isq) y = *reinterpret_cast<const u32x4*>(o + ch * kVec);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) {
-          acc = fmaf(__uint_as_float(x[e]), __uint_as_float(y[e]), acc);
-        } else {
-          const float x0 = Elt<T>::lo(x[e]), x1 = Elt<T>::hi(x[e]);
-          acc = fmaf(x0, Elt<T>::lo(y[e]), acc);
-          acc = fmaf(x1, Elt<T>::hi(y[e]), acc);
-          sq = fmaf(x0, x0, fmaf(x1, x1, sq));
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) {
-    acc += __shfl_xor(acc, d);
-    sq += __shfl_xor(sq, d);
-  }
-  if (isq && sub == 0) p.delta[id % p.hq * p.nq + id / p.hq] = acc;
-  if (sizeof(T) == 2 && bound) {
-    float mq = isq && sq < INFINITY ? sq : 0.f, mv = isv && sq < INFINITY ? sq : 0.f;
-#pragma unroll
-    for (int d = 16; d < 64; d <<= 1) {
-      mq = fmaxf(mq, __shfl_xor(mq, d));
-      mv = fmaxf(mv, __shfl_xor(mv, d));
-    }
-    if ((threadIdx.x & 63) == 0) {
-      if (mq > 0.f) atomicMax(&bound[0], __float_as_uint(mq));
-      if (mv > 0.f) atomicMax(&bound[1], __float_as_uint(mv));
-    }
-  }
-}
-
-// clears the two bounds before the maxima
-static __global__ void bound_clear_kernel(uint32_t* bound) {
-  if (threadIdx.x < 2) bound[threadIdx.x] = 0u;
-}
-
-// Power of two for dS in fp16: |dS| <= |dP - delta| <= 2 |dout row| |v row| (out lies within the values it averages),
-// so with b2 = max |dout row|^2 max |v row|^2 < 2^e the scaled dS stays below 2^(1 + e/2 + s) <= 2^15.5 < 65504 for
-// s = 14 - floor(e / 2).  The rest of fp16's range (steps of 2^-24) is then all below the largest possible entry.
-template <typename T>
-__device__ __forceinline__ int ds_exp(const Params& p) {
-  if constexpr (kPExp<T> == 0) {
-    return 0;
-  } else {
-    const float b2 = __uint_as_float(p.bound[0]) * __uint_as_float(p.bound[1]);
-    if (!(b2 > 0.f) || !(b2 < INFINITY)) return 0;
-    int e;
-    (void)frexpf(b2, &e);
-    const int s = 14 - (e >> 1);
-    return s < -30 ? -30 : (s > 60 ? 60 : s);
-  }
-}
 
 // Loads resident columns (rows of a [n][head][d] tensor) as B fragments
 template <typename T, int DP>
@@ -659,20 +383,412 @@ __device__ __forceinline__ void store_cols(T* dst, float* part, const f32x16 (&o
     }
 }
 
-template <typename T, int DP, int NW, int QB, bool MASK>
-__global__ void __launch_bounds__(NW * 64) dq_kernel(Params p) {
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+
+// Forward exponentials are taken against a reference at most kSlack (a power of two's exponent) below the row's
+// maximum, with an offset that keeps the largest inside fp16's 65504.
+template <typename T>
+constexpr int kFwdExp = __is_same(T, _Float16) ? 8 : 0;
+constexpr float kSlack = 7.f;
+
+// Two forms.  Rows: each wave owns QB * 32 query columns and the workgroup's waves share the streamed tiles, double
+// buffered in LDS.  FEW (a sample's rows fit 32 columns: single tokens while serving): the waves share the columns and
+// take the tiles in turn, each through an LDS tile of its own with no barrier, and join their sums at the end.
+template <typename T, int DP, int NW, int QB, bool MASK, bool FEW>
+__global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd_occ) fwd_kernel(Params p) {
   using TL = TileOf<T, DP>;
   using E = Elt<T>;
-  constexpr int NT = NW * 64, TC = NW * QB * 32;
-  __shared__ __align__(16) char lk[2][TL::kBytes];
-  __shared__ __align__(16) char lv[2][TL::kBytes];
-  __shared__ unsigned long long lvalid[2];
+  constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * QB * 32, BUFS = FEW ? NW : 2;
+  __shared__ __align__(16) char lds[2 * BUFS * TL::kBytes];
+  __shared__ unsigned long long lvalid[BUFS];
+  __shared__ float lml[FEW ? 2 * NW * 32 : 1];
   const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
   if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
   const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
   Segment sg;
   if (!find_segment(p.qoff, p.nq, p.koff, p.nk, p.batch, p.G, TC, tile, &sg)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
+  const int dchunks = p.d / TL::kVec;
+  // the running maximum is taken on unscaled scores: a negative scale's sign goes into the queries (exactly), and a
+  // scale of zero clears them (a masked score's -inf times 0 would be NaN)
+  const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
+  const uint32_t clear = p.scale == 0.f ? 0u : ~0u;
+  const uint32_t flip = p.scale < 0.f ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
+
+  // this lane's query columns
+  int64_t row[QB];
+  int head[QB];
+  bool live[QB];
+  u32x4 qf[QB][TL::kFrags];
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    const uint32_t r = uint32_t(sg.tile) * TC + (FEW ? 0 : (wave * QB + b) * 32) + (lane & 31);
+    live[b] = r < uint32_t(sg.len) * uint32_t(p.G);
+    const uint32_t rc = live[b] ? r : 0u, tok = div_g(rc, p);
+    row[b] = sg.begin + tok;
+    head[b] = hk * p.G + int(rc - tok * uint32_t(p.G));
+    load_cols<T, DP>(static_cast<const T*>(p.q) + row[b] * p.q_row + head[b] * p.q_head, live[b], dchunks, qf[b]);
+#pragma unroll
+    for (int f = 0; f < TL::kFrags; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qf[b][f][e] = (qf[b][f][e] & clear) ^ flip;
+  }
+
+  f32x16 o[QB][TL::kBlocks];
+  float m[QB], l[QB];
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    m[b] = -INFINITY;
+    l[b] = 0.f;
+#pragma unroll
+    for (int d = 0; d < TL::kBlocks; ++d) o[b][d] = f32x16{};
+  }
+
+  int t0, t1;
+  split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
+  constexpr int step = FEW ? NW : 1;
+  if (FEW) t0 += wave;
+  const T* kp = static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head;
+  const T* vp = static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head;
+  const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
+  Stage<T, DP, NT> sk, sv;
+  sk.init(uint32_t(p.k_row * int64_t(sizeof(T))), dchunks);
+  sv.init(uint32_t(p.v_row * int64_t(sizeof(T))), dchunks);
+  uint8_t keep[Stage<T, DP, NT>::N];
+  bool kept = false;  // the key of streamed row `lane`
+  auto load = [&](int t) {
+    const int64_t k0 = int64_t(t) * TL::kRows;
+    const int rows = sg.other_len - t * TL::kRows;
+    sk.load(kp + k0 * p.k_row, rows, p.k_row * int64_t(sizeof(T)), head_bytes);
+    sv.load(vp + k0 * p.v_row, rows, p.v_row * int64_t(sizeof(T)), head_bytes);
+    if constexpr (MASK) {
+      const uint8_t* mp = p.mask + sg.other + k0;
+#pragma unroll
+      for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
+        const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
+        keep[i] = (r < rows && r < TL::kRows) ? mp[r] : 0;
+      }
+      kept = lane < rows && lane < TL::kRows && mp[lane] != 0;
+    }
+  };
+  if (t0 < t1) load(t0);
+  for (int t = t0, n = 0; t < t1; t += step, ++n) {
+    const int buf = FEW ? wave : n & 1;
+    char* lk = lds + buf * 2 * TL::kBytes;
+    char* lv = lk + TL::kBytes;
+    constexpr uint64_t kAll = ~0ull >> (64 - TL::kRows);
+    uint64_t valid = 0;
+    if constexpr (MASK) {
+      sk.clear(keep);
+      sv.clear(keep);
+      valid = __ballot(kept);
+      if (!FEW && threadIdx.x == 0) lvalid[buf] = valid;
+    }
+    sk.store(lk);
+    sv.store(lv);
+    if constexpr (FEW)
+      wave_fence();  // LDS serves a wave's accesses in order
+    else
+      __syncthreads();
+    const int rows = sg.other_len - t * TL::kRows;
+    if constexpr (!MASK)
+      valid = rows >= TL::kRows ? kAll : (1ull << rows) - 1;
+    else if constexpr (!FEW)
+      valid = lvalid[buf];
+    if (t + step < t1) load(t + step);
+    if (MASK && valid == 0) continue;
+
+    f32x16 s[QB][TL::kGroups];
+#pragma unroll
+    for (int kb = 0; kb < TL::kGroups; ++kb) {
+#pragma unroll
+      for (int b = 0; b < QB; ++b) s[b][kb] = f32x16{};
+#pragma unroll
+      for (int f = 0; f < TL::kFrags; ++f) {
+        const u32x4 a = TL::rows(lk, 32 * kb, f);
+#pragma unroll
+        for (int b = 0; b < QB; ++b) s[b][kb] = E::mma(a, qf[b][f], s[b][kb]);
+      }
+    }
+    if (valid != kAll) {
+#pragma unroll
+      for (int kb = 0; kb < TL::kGroups; ++kb) {
+        const uint32_t w = uint32_t(valid >> (32 * kb)) >> (4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool on = (w >> (8 * (r / 4) + r % 4)) & 1u;
+#pragma unroll
+          for (int b = 0; b < QB; ++b) s[b][kb][r] = on ? s[b][kb][r] : -INFINITY;
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      float mx = s[b][0][0];
+#pragma unroll
+      for (int kb = 0; kb < TL::kGroups; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][kb][r]);
+      mx = fmaxf(mx, half_swap(mx)) * c;
+      // The reference point of the exponentials follows the running maximum only when a row's has grown past what the
+      // type holds (2^kSlack): any reference gives the same quotient, and most tiles then skip the rescaling.
+      if (__any(mx > m[b] + kSlack)) {
+        const float mn = fmaxf(m[b], mx);
+        const float al = m[b] == mn ? 1.f : __builtin_amdgcn_exp2f(m[b] - mn);  // -inf stays: nothing attended yet
+        m[b] = mn;
+        l[b] *= al;
+#pragma unroll
+        for (int d = 0; d < TL::kBlocks; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[b][d][r] *= al;
+      }
+      const float ref = m[b] == -INFINITY ? 0.f : m[b];
+      const float sh = float(kFwdExp<T>) - ref;
+#pragma unroll
+      for (int kb = 0; kb < TL::kGroups; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[b][kb][r], c, sh));
+          s[b][kb][r] = e;
+          l[b] += e;
+        }
+    }
+#pragma unroll
+    for (int kb = 0; kb < TL::kGroups; ++kb)
+#pragma unroll
+      for (int st = 0; st < E::kSteps; ++st) {
+        u32x4 pf[QB];
+#pragma unroll
+        for (int b = 0; b < QB; ++b) pf[b] = E::pack(s[b][kb], st);
+#pragma unroll
+        for (int d = 0; d < TL::kBlocks; ++d) {
+          const u32x4 a = TL::cols(lv, 32 * kb, st, d);
+#pragma unroll
+          for (int b = 0; b < QB; ++b) o[b][d] = E::mma(a, pf[b], o[b][d]);
+        }
+      }
+  }
+
+  if constexpr (FEW) {
+    // The waves' references differ: each wave's sums are brought to the largest, then added in wave order.  2 NW
+    // threads share a column's elements.
+    float total = l[0] + half_swap(l[0]);
+    if (half == 0) {
+      lml[wave * 32 + lane] = m[0];
+      lml[(NW + wave) * 32 + lane] = total;
+    }
+    __syncthreads();
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, lml[w * 32 + (lane & 31)]);
+    const float al = m[0] == mx ? 1.f : __builtin_amdgcn_exp2f(m[0] - mx);
+    float* mine = reinterpret_cast<float*>(lds) + wave * DP * 33;
+#pragma unroll
+    for (int d = 0; d < TL::kBlocks; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mine[(32 * d + 8 * (r / 4) + 4 * half + r % 4) * 33 + (lane & 31)] = o[0][d][r] * al;
+    __syncthreads();
+    constexpr int TPC = 2 * NW;
+    const int col = threadIdx.x / TPC, e0 = threadIdx.x % TPC;
+    const uint32_t r = uint32_t(sg.tile) * TC + col;
+    if (r >= uint32_t(sg.len) * uint32_t(p.G)) return;
+    const uint32_t tok = div_g(r, p);
+    const int64_t orow = sg.begin + tok;
+    const int ohead = hk * p.G + int(r - tok * uint32_t(p.G));
+    mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, lml[w * 32 + col]);
+    total = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float mw = lml[w * 32 + col];
+      total += lml[(NW + w) * 32 + col] * (mw == mx ? 1.f : __builtin_amdgcn_exp2f(mw - mx));
+    }
+    const bool some = total != 0.f;  // NaN counts
+    const float inv = p.nsplit > 1 ? 1.f : (some ? 1.f / total : 0.f);
+    const int64_t at = (int64_t(split) * p.nq + orow) * p.hq + ohead;
+    for (int e = e0; e < p.d; e += TPC) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(lds)[w * DP * 33 + e * 33 + col];
+      if (p.nsplit > 1)
+        p.part_a[at * p.d + e] = v;
+      else
+        static_cast<T*>(p.o)[(orow * p.hq + ohead) * p.d + e] = T(v * inv);
+    }
+    if (e0 == 0) {
+      if (p.nsplit > 1) {
+        p.part_b[2 * at] = mx;
+        p.part_b[2 * at + 1] = total;
+      } else {
+        p.lse[int64_t(ohead) * p.nq + orow] = some ? (mx - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+      }
+    }
+    return;
+  }
+
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    const float total = l[b] + half_swap(l[b]);
+    if (!live[b]) continue;
+    const bool some = total != 0.f;  // NaN counts
+    if (p.nsplit > 1) {
+      const int64_t at = (int64_t(split) * p.nq + row[b]) * p.hq + head[b];
+      if (half == 0) {
+        p.part_b[2 * at] = m[b];
+        p.part_b[2 * at + 1] = total;
+      }
+      store_cols<T, DP>(nullptr, p.part_a + at * p.d, o[b], p.d, 1.f);
+      continue;
+    }
+    if (half == 0)
+      p.lse[int64_t(head[b]) * p.nq + row[b]] = some ? (m[b] - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+    store_cols<T, DP>(static_cast<T*>(p.o) + (row[b] * p.hq + head[b]) * p.d, nullptr, o[b], p.d, some ? 1.f / total : 0.f);
+  }
+}
+
+constexpr int kMaxSplit = 128;
+
+// Joins the splits of the forward pass: a workgroup per (row, head).  The splits' weights are formed once, side by
+// side; the four waves then add their splits' rows and the wave sums are added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
+  __shared__ float lw[kMaxSplit], lsum[4][SSC_MAX_HEAD_DIM];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rh = blockIdx.x, n = p.nq * p.hq;
+  // every wave forms the same maximum and sum
+  float mx = -INFINITY, ms[kMaxSplit / 64], ls[kMaxSplit / 64];
+#pragma unroll
+  for (int i = 0; i < kMaxSplit / 64; ++i) {
+    const int s = lane + 64 * i;
+    ms[i] = s < p.nsplit ? p.part_b[2 * (s * n + rh)] : -INFINITY;
+    ls[i] = s < p.nsplit ? p.part_b[2 * (s * n + rh) + 1] : 0.f;
+    mx = fmaxf(mx, ms[i]);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplit / 64; ++i) {
+    const float w = ms[i] == mx ? 1.f : __builtin_amdgcn_exp2f(ms[i] - mx);
+    total += w * ls[i];
+    if (wave == 0) lw[lane + 64 * i] = w;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  __syncthreads();
+  float acc[2] = {0.f, 0.f};
+#pragma unroll 4
+  for (int s = wave; s < p.nsplit; s += 4) {
+    const float w = lw[s];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 64 * e < p.d) acc[e] = fmaf(w, p.part_a[(s * n + rh) * p.d + lane + 64 * e], acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) lsum[wave][lane + 64 * e] = acc[e];
+  __syncthreads();
+  const bool some = total != 0.f;
+  const float inv = some ? 1.f / total : 0.f;
+  const int e = threadIdx.x;
+  if (e < p.d) static_cast<T*>(p.o)[rh * p.d + e] = T(((lsum[0][e] + lsum[1][e]) + (lsum[2][e] + lsum[3][e])) * inv);
+  if (e == 0) p.lse[(rh % p.hq) * p.nq + rh / p.hq] = some ? (mx - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+
+// fp16: the largest |dout row|^2 and |v row|^2 (maxima: any order gives the same), which bound dS for its scaling to
+// fp16's range.  16 lanes a (row, head); infinite or NaN rows are left out and spoil the results they reach.
+template <typename T>
+__global__ void __launch_bounds__(256) bound_kernel(Params p, uint32_t* bound) {
+  const int sub = threadIdx.x & 15, chunks = p.d / 8;
+  const int64_t nd = p.nq * p.hq, nv = p.nk * p.hk, step = int64_t(gridDim.x) * 16;
+  float mq = 0.f, mv = 0.f;
+  const int64_t first = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  // whole waves iterate together: the groups' sums cross lanes
+  for (int64_t base = int64_t(blockIdx.x) * 16; base < nd + nv; base += step) {
+    const int64_t id = first + (base - int64_t(blockIdx.x) * 16), vi = id - nd;
+    const bool isq = id < nd, isv = !isq && vi < nv && (!p.mask || p.mask[vi / p.hk]);
+    float sq = 0.f;
+    if (isq || isv) {
+      const T* a = isq ? static_cast<const T*>(p.dout) + id * p.d
+                       : static_cast<const T*>(p.v) + vi / p.hk * p.v_row + vi % p.hk * p.v_head;
+      for (int ch = sub; ch < chunks; ch += 16) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(a + ch * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sq = Elt<T>::dot(x[e], x[e], sq);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) sq += __shfl_xor(sq, d);
+    if (sq < INFINITY) {
+      if (isq) mq = fmaxf(mq, sq);
+      if (isv) mv = fmaxf(mv, sq);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) {
+    mq = fmaxf(mq, __shfl_xor(mq, d));
+    mv = fmaxf(mv, __shfl_xor(mv, d));
+  }
+  if ((threadIdx.x & 63) == 0) {
+    if (mq > 0.f) atomicMax(&bound[0], __float_as_uint(mq));
+    if (mv > 0.f) atomicMax(&bound[1], __float_as_uint(mv));
+  }
+}
+
+// clears the two bounds before the maxima
+static __global__ void bound_clear_kernel(uint32_t* bound) {
+  if (threadIdx.x < 2) bound[threadIdx.x] = 0u;
+}
+
+// Power of two for dS in fp16: |dS| <= |dP - delta| <= 2 |dout row| |v row| (out lies within the values it averages),
+// so with b2 = max |dout row|^2 max |v row|^2 < 2^e the scaled dS stays below 2^(1 + e/2 + s) <= 2^15.5 < 65504 for
+// s = 14 - floor(e / 2).  The rest of fp16's range (steps of 2^-24) is then all below the largest possible entry.
+template <typename T>
+__device__ __forceinline__ int ds_exp(const Params& p) {
+  if constexpr (kPExp<T> == 0) {
+    return 0;
+  } else {
+    const float b2 = __uint_as_float(p.bound[0]) * __uint_as_float(p.bound[1]);
+    if (!(b2 > 0.f) || !(b2 < INFINITY)) return 0;
+    int e;
+    (void)frexpf(b2, &e);
+    const int s = 14 - (e >> 1);
+    return s < -30 ? -30 : (s > 60 ? 60 : s);
+  }
+}
+
+// v times dS's power of two, which only fp16 has
+template <typename T>
+__device__ __forceinline__ float scaled(float v, float mul) {
+  return kPExp<T> == 0 ? v : v * mul;
+}
+
+// dQ, and the exact delta.  The forward result that delta = dout . out is formed from was rounded to 16 bits, and that
+// error meets every key of the row with one sign: where attention is peaked it outweighs dS itself.  The sum of a row's
+// dS is zero, so the sum e of the dS formed with the rounded delta is the error: delta + e is exact to fp32, and
+// dq = scale (sum dS k - e sum P k).  The second sum is one more product on operands that are at hand; the dK pass
+// reads the corrected delta.  fp32 results need none of it.
+template <typename T, int DP, int NW, int QB, bool MASK, bool FEW>
+__global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
+  using TL = TileOf<T, DP>;
+  using E = Elt<T>;
+  constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * QB * 32, BUFS = FEW ? NW : 2;
+  constexpr bool kFix = sizeof(T) == 2;
+  __shared__ __align__(16) char lds[2 * BUFS * TL::kBytes];
+  __shared__ unsigned long long lvalid[BUFS];
+  __shared__ float le[FEW ? (NW + 1) * 32 : 1];  // the waves' sums of dS, then delta
+  const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
+  if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
+  const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
+  Segment sg;
+  if (!find_segment(p.qoff, p.nq, p.koff, p.nk, p.batch, p.G, TC, tile, &sg)) return;
+  const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
   const int dchunks = p.d / TL::kVec;
   const float c = p.scale * kLog2e;
   const int dse = ds_exp<T>(p);
@@ -682,65 +798,89 @@ __global__ void __launch_bounds__(NW * 64) dq_kernel(Params p) {
   int head[QB];
   bool live[QB];
   u32x4 qf[QB][TL::kFrags], df[QB][TL::kFrags];
-  float sh[QB], del[QB];
-  f32x16 acc[QB][TL::kBlocks];
+  float sh[QB], del[QB], esum[QB];
+  f32x16 acc[QB][TL::kBlocks], mean[kFix ? QB : 1][TL::kBlocks];
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
-    const uint32_t r = uint32_t(sg.tile) * TC + (wave * QB + b) * 32 + (lane & 31);
+    const uint32_t r = uint32_t(sg.tile) * TC + (FEW ? 0 : (wave * QB + b) * 32) + (lane & 31);
     live[b] = r < uint32_t(sg.len) * uint32_t(p.G);
     const uint32_t rc = live[b] ? r : 0u, tok = div_g(rc, p);
     row[b] = sg.begin + tok;
     head[b] = hk * p.G + int(rc - tok * uint32_t(p.G));
     load_cols<T, DP>(static_cast<const T*>(p.q) + row[b] * p.q_row + head[b] * p.q_head, live[b], dchunks, qf[b]);
     load_cols<T, DP>(static_cast<const T*>(p.dout) + (row[b] * p.hq + head[b]) * p.d, live[b], dchunks, df[b]);
-    const int64_t at = int64_t(head[b]) * p.nq + row[b];
-    const float lse = live[b] ? p.lse[at] : -INFINITY;
-    sh[b] = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;  // rows with no key: probabilities 0
-    del[b] = live[b] ? p.delta[at] : 0.f;
+    u32x4 of[TL::kFrags];
+    load_cols<T, DP>(static_cast<const T*>(p.out) + (row[b] * p.hq + head[b]) * p.d, live[b], dchunks, of);
+    float dot = 0.f;
 #pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) acc[b][d] = f32x16{};
+    for (int f = 0; f < TL::kFrags; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dot = E::dot(df[b][f][e], of[f][e], dot);
+    del[b] = dot + half_swap(dot);
+    const float lse = live[b] ? p.lse[int64_t(head[b]) * p.nq + row[b]] : -INFINITY;
+    sh[b] = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;  // rows with no key: probabilities 0
+    esum[b] = 0.f;
+#pragma unroll
+    for (int d = 0; d < TL::kBlocks; ++d) {
+      acc[b][d] = f32x16{};
+      if constexpr (kFix) mean[b][d] = f32x16{};
+    }
   }
 
   int t0, t1;
-  split_range(sg.other_len, split, p.nsplit, &t0, &t1);
+  split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
+  constexpr int step = FEW ? NW : 1;
+  if (FEW) t0 += wave;
   const T* kp = static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head;
   const T* vp = static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head;
+  const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
   Stage<T, DP, NT> sk, sv;
+  sk.init(uint32_t(p.k_row * int64_t(sizeof(T))), dchunks);
+  sv.init(uint32_t(p.v_row * int64_t(sizeof(T))), dchunks);
   uint8_t keep[Stage<T, DP, NT>::N];
   bool kept = false;
   auto load = [&](int t) {
-    const int64_t k0 = int64_t(t) * kTile;
-    const int rows = sg.other_len - t * kTile;
-    sk.load(rows, dchunks, [&](int r) { return kp + (k0 + r) * p.k_row; });
-    sv.load(rows, dchunks, [&](int r) { return vp + (k0 + r) * p.v_row; });
+    const int64_t k0 = int64_t(t) * TL::kRows;
+    const int rows = sg.other_len - t * TL::kRows;
+    sk.load(kp + k0 * p.k_row, rows, p.k_row * int64_t(sizeof(T)), head_bytes);
+    sv.load(vp + k0 * p.v_row, rows, p.v_row * int64_t(sizeof(T)), head_bytes);
     if constexpr (MASK) {
       const uint8_t* mp = p.mask + sg.other + k0;
 #pragma unroll
       for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
         const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
-        keep[i] = (r < rows && r < kTile) ? mp[r] : 0;
+        keep[i] = (r < rows && r < TL::kRows) ? mp[r] : 0;
       }
-      kept = lane < rows && mp[lane] != 0;
+      kept = lane < rows && lane < TL::kRows && mp[lane] != 0;
     }
   };
   if (t0 < t1) load(t0);
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
+  for (int t = t0, n = 0; t < t1; t += step, ++n) {
+    const int buf = FEW ? wave : n & 1;
+    char* lk = lds + buf * 2 * TL::kBytes;
+    char* lv = lk + TL::kBytes;
+    constexpr uint64_t kAll = ~0ull >> (64 - TL::kRows);
+    uint64_t valid = 0;
     if constexpr (MASK) {
       sk.clear(keep);
       sv.clear(keep);
-      const uint64_t w = __ballot(kept);
-      if (threadIdx.x == 0) lvalid[buf] = w;
+      valid = __ballot(kept);
+      if (!FEW && threadIdx.x == 0) lvalid[buf] = valid;
     }
-    sk.store(lk[buf]);
-    sv.store(lv[buf]);
-    __syncthreads();
-    const int rows = sg.other_len - t * kTile;
-    uint64_t valid = rows >= kTile ? ~0ull : (1ull << rows) - 1;
-    if constexpr (MASK) valid = lvalid[buf];
-    if (t + 1 < t1) load(t + 1);
+    sk.store(lk);
+    sv.store(lv);
+    if constexpr (FEW)
+      wave_fence();
+    else
+      __syncthreads();
+    const int rows = sg.other_len - t * TL::kRows;
+    if constexpr (!MASK)
+      valid = rows >= TL::kRows ? kAll : (1ull << rows) - 1;
+    else if constexpr (!FEW)
+      valid = lvalid[buf];
+    if (t + step < t1) load(t + step);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < TL::kGroups; ++kb) {
       const uint32_t vw = uint32_t(valid >> (32 * kb));
       if (vw == 0) continue;
       f32x16 s[QB], dp[QB];
@@ -748,7 +888,7 @@ __global__ void __launch_bounds__(NW * 64) dq_kernel(Params p) {
       for (int b = 0; b < QB; ++b) s[b] = dp[b] = f32x16{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
-        const u32x4 a = TL::rows(lk[buf], 32 * kb, f), v = TL::rows(lv[buf], 32 * kb, f);
+        const u32x4 a = TL::rows(lk, 32 * kb, f), v = TL::rows(lv, 32 * kb, f);
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
           s[b] = E::mma(a, qf[b][f], s[b]);
@@ -758,10 +898,7 @@ __global__ void __launch_bounds__(NW * 64) dq_kernel(Params p) {
 #pragma unroll
       for (int b = 0; b < QB; ++b)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float pr = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, sh[b]));
-          s[b][r] = pr * ((dp[b][r] - del[b]) * dsmul);
-        }
+        for (int r = 0; r < 16; ++r) s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, sh[b]));
       if (~vw != 0) {
         const uint32_t w = vw >> (4 * half);
 #pragma unroll
@@ -772,37 +909,166 @@ __global__ void __launch_bounds__(NW * 64) dq_kernel(Params p) {
         }
       }
 #pragma unroll
-      for (int st = 0; st < E::kSteps; ++st) {
-        u32x4 pf[QB];
+      for (int b = 0; b < QB; ++b)
 #pragma unroll
-        for (int b = 0; b < QB; ++b) pf[b] = E::pack(s[b], st);
+        for (int r = 0; r < 16; ++r) {
+          dp[b][r] = s[b][r] * scaled<T>(dp[b][r] - del[b], dsmul);
+          if constexpr (kFix) esum[b] += dp[b][r];
+        }
+#pragma unroll
+      for (int st = 0; st < E::kSteps; ++st) {
+        u32x4 pf[QB], sf[QB];
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+          sf[b] = E::pack(dp[b], st);
+          if constexpr (kFix) pf[b] = E::pack(s[b], st);
+        }
 #pragma unroll
         for (int d = 0; d < TL::kBlocks; ++d) {
-          const u32x4 a = TL::cols(lk[buf], 32 * kb, st, d);
+          const u32x4 a = TL::cols(lk, 32 * kb, st, d);
 #pragma unroll
-          for (int b = 0; b < QB; ++b) acc[b][d] = E::mma(a, pf[b], acc[b][d]);
+          for (int b = 0; b < QB; ++b) {
+            acc[b][d] = E::mma(a, sf[b], acc[b][d]);
+            if constexpr (kFix) mean[b][d] = E::mma(a, pf[b], mean[b][d]);
+          }
         }
       }
     }
   }
-  const float f = ldexpf(p.scale, -dse);
+  // dS carries 2^dse and P 2^kPExp: e in units of delta is esum 2^-dse
+  const float f = ldexpf(p.scale, -dse), unit = ldexpf(1.f, -dse), punit = ldexpf(1.f, dse - kPExp<T>);
+  if constexpr (FEW) {
+    // the waves' sums, added in wave order; 2 NW threads share a column's elements
+    float* all = reinterpret_cast<float*>(lds);
+    float* mine = all + wave * DP * 33;
+    const float e = kFix ? esum[0] + half_swap(esum[0]) : 0.f;
+    if (half == 0) {
+      le[wave * 32 + lane] = e;
+      if (wave == 0) le[NW * 32 + lane] = del[0];
+    }
+    constexpr int TPC = 2 * NW;
+    const int col = threadIdx.x / TPC, e0 = threadIdx.x % TPC;
+    const uint32_t r = uint32_t(sg.tile) * TC + col;
+    const bool here = r < uint32_t(sg.len) * uint32_t(p.G);
+    const uint32_t tok = div_g(r, p);
+    const int64_t orow = sg.begin + tok;
+    const int ohead = hk * p.G + int(r - tok * uint32_t(p.G));
+    const int64_t rh = orow * p.hq + ohead, sp = int64_t(split) * p.nq * p.hq + rh;
+    float sums[DP / TPC] = {};
+    float es = 0.f;
+#pragma unroll
+    for (int pass = 0; pass < (kFix ? 2 : 1); ++pass) {
+      __syncthreads();  // the tiles, or the first pass's sums, are read out
+#pragma unroll
+      for (int d = 0; d < TL::kBlocks; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          mine[(32 * d + 8 * (i / 4) + 4 * half + i % 4) * 33 + (lane & 31)] = pass == 0 ? acc[0][d][i] : mean[0][d][i];
+      __syncthreads();
+      if (pass == 0) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) es += le[w * 32 + col];
+        es *= unit;
+      }
+#pragma unroll
+      for (int i = 0; i < DP / TPC; ++i) {
+        const int x = e0 + TPC * i;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += all[w * DP * 33 + x * 33 + col];
+        if (p.nsplit > 1 && here && x < p.d && p.dq) {
+          if (pass == 0)
+            p.part_a[sp * p.d + x] = v * f;
+          else
+            p.part_b[sp * p.d + x] = v * ldexpf(p.scale, -kPExp<T>);
+        }
+        sums[i] = pass == 0 ? v : fmaf(-es * punit, v, sums[i]);
+      }
+    }
+    if (!here) return;
+    if (e0 == 0 && p.nsplit > 1) {
+      if constexpr (kFix) p.part_e[sp] = es;
+    }
+    if (p.nsplit == 1 && p.dq) {
+#pragma unroll
+      for (int i = 0; i < DP / TPC; ++i)
+        if (e0 + TPC * i < p.d) static_cast<T*>(p.dq)[rh * p.d + e0 + TPC * i] = T(sums[i] * f);
+    }
+    if (e0 == 0 && split == 0) p.delta[int64_t(ohead) * p.nq + orow] = le[NW * 32 + col] + (p.nsplit > 1 ? 0.f : es);
+    return;
+  }
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
+    const float e = kFix ? esum[b] + half_swap(esum[b]) : 0.f;
     if (!live[b]) continue;
-    const int64_t at = (row[b] * p.hq + head[b]) * p.d;
-    store_cols<T, DP>(static_cast<T*>(p.dq) + at, p.nsplit > 1 ? p.part_a + int64_t(split) * p.nq * p.hq * p.d + at : nullptr,
-                      acc[b], p.d, f);
+    const int64_t rh = row[b] * p.hq + head[b], at = rh * p.d;
+    if (p.nsplit > 1) {
+      const int64_t sp = int64_t(split) * p.nq * p.hq;
+      if (p.dq) {
+        store_cols<T, DP>(nullptr, p.part_a + sp * p.d + at, acc[b], p.d, f);
+        if constexpr (kFix) store_cols<T, DP>(nullptr, p.part_b + sp * p.d + at, mean[b], p.d, ldexpf(p.scale, -kPExp<T>));
+      }
+      if (half == 0) {
+        if constexpr (kFix) p.part_e[sp + rh] = e * unit;
+        if (split == 0) p.delta[int64_t(head[b]) * p.nq + row[b]] = del[b];
+      }
+      continue;
+    }
+    if (half == 0) p.delta[int64_t(head[b]) * p.nq + row[b]] = del[b] + e * unit;
+    if (!p.dq) continue;
+    if constexpr (kFix)
+#pragma unroll
+      for (int d = 0; d < TL::kBlocks; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[b][d][r] = fmaf(-(e * unit) * punit, mean[b][d][r], acc[b][d][r]);
+    store_cols<T, DP>(static_cast<T*>(p.dq) + at, nullptr, acc[b], p.d, f);
   }
 }
 
-template <typename T, int DP, int NW, bool MASK>
-__global__ void __launch_bounds__(NW * 64) dkv_kernel(Params p) {
+// Joins the splits of dQ: a workgroup per (row, head), its waves taking the splits in turn.  e is the sum of the
+// splits' sums of dS (see dq_kernel).
+template <typename T>
+__global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
+  __shared__ float la[4][SSC_MAX_HEAD_DIM], lm[4][SSC_MAX_HEAD_DIM];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rh = blockIdx.x, n = p.nq * p.hq;
+  float e = 0.f;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < kMaxSplit / 64; ++i)
+      if (lane + 64 * i < p.nsplit) e += p.part_e[(lane + 64 * i) * n + rh];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) e += __shfl_xor(e, d);
+    if (threadIdx.x == 0) p.delta[(rh % p.hq) * p.nq + rh / p.hq] += e;
+  }
+  if (!p.dq) return;
+  float a[2] = {0.f, 0.f}, m[2] = {0.f, 0.f};
+#pragma unroll 4
+  for (int s = wave; s < p.nsplit; s += 4)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 64 * i < p.d) {
+        a[i] += p.part_a[(s * n + rh) * p.d + lane + 64 * i];
+        if constexpr (sizeof(T) == 2) m[i] += p.part_b[(s * n + rh) * p.d + lane + 64 * i];
+      }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) la[wave][lane + 64 * i] = a[i], lm[wave][lane + 64 * i] = m[i];
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i < p.d) {
+    const float as = (la[0][i] + la[1][i]) + (la[2][i] + la[3][i]), mm = (lm[0][i] + lm[1][i]) + (lm[2][i] + lm[3][i]);
+    static_cast<T*>(p.dq)[rh * p.d + i] = T(fmaf(-e, mm, as));
+  }
+}
+
+template <typename T, int DP, int NW, int KB, bool MASK>
+__global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
   using TL = TileOf<T, DP>;
   using E = Elt<T>;
-  constexpr int NT = NW * 64, TC = NW * 32;
+  constexpr int NT = NW * 64, TC = NW * KB * 32;
   __shared__ __align__(16) char lq[2][TL::kBytes];
   __shared__ __align__(16) char ld[2][TL::kBytes];
-  __shared__ __align__(16) float lsh[2][kTile], ldel[2][kTile];
+  __shared__ __align__(16) float lsh[2][TL::kRows], ldel[2][TL::kRows];
   const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
   if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
   const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
@@ -814,95 +1080,123 @@ __global__ void __launch_bounds__(NW * 64) dkv_kernel(Params p) {
   const int dse = ds_exp<T>(p);
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);
 
-  const int col = sg.tile * TC + wave * 32 + (lane & 31);
-  const bool live = col < sg.len;
-  const int64_t row = sg.begin + (live ? col : 0);
-  const bool on = live && (!MASK || p.mask[row] != 0);
-  u32x4 kf[TL::kFrags], vf[TL::kFrags];
-  load_cols<T, DP>(static_cast<const T*>(p.k) + row * p.k_row + hk * p.k_head, on, dchunks, kf);
-  load_cols<T, DP>(static_cast<const T*>(p.v) + row * p.v_row + hk * p.v_head, on, dchunks, vf);
-  f32x16 dk[TL::kBlocks], dv[TL::kBlocks];
+  bool live[KB], on[KB];
+  int64_t row[KB];
+  u32x4 kf[KB][TL::kFrags], vf[KB][TL::kFrags];
+  f32x16 dk[KB][TL::kBlocks], dv[KB][TL::kBlocks];
 #pragma unroll
-  for (int d = 0; d < TL::kBlocks; ++d) dk[d] = dv[d] = f32x16{};
+  for (int b = 0; b < KB; ++b) {
+    const int col = sg.tile * TC + (wave * KB + b) * 32 + (lane & 31);
+    live[b] = col < sg.len;
+    row[b] = sg.begin + (live[b] ? col : 0);
+    on[b] = live[b] && (!MASK || p.mask[row[b]] != 0);
+    load_cols<T, DP>(static_cast<const T*>(p.k) + row[b] * p.k_row + hk * p.k_head, on[b], dchunks, kf[b]);
+    load_cols<T, DP>(static_cast<const T*>(p.v) + row[b] * p.v_row + hk * p.v_head, on[b], dchunks, vf[b]);
+#pragma unroll
+    for (int d = 0; d < TL::kBlocks; ++d) dk[b][d] = dv[b][d] = f32x16{};
+  }
+  // waves whose columns all lie past the sample's keys only help to stage
+  const bool busy = sg.tile * TC + wave * KB * 32 < sg.len;
 
-  const int qrows = sg.other_len * p.G;  // (token, head) rows
+  // the sample's queries, head after head of the group: step t is head t / tiles, tile t % tiles
+  const int tiles = (sg.other_len + TL::kRows - 1) / TL::kRows;
   int t0, t1;
-  split_range(qrows, split, p.nsplit, &t0, &t1);
+  split_range(tiles * p.G, split, p.nsplit, &t0, &t1);
   const T* qp = static_cast<const T*>(p.q) + sg.other * p.q_row + int64_t(hk) * p.G * p.q_head;
   const T* dp_ = static_cast<const T*>(p.dout) + (sg.other * p.hq + int64_t(hk) * p.G) * p.d;
+  const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
+  const int64_t q_bytes = p.q_row * int64_t(sizeof(T)), d_bytes = int64_t(p.hq) * head_bytes;
   Stage<T, DP, NT> sq, sd;
+  sq.init(uint32_t(q_bytes), dchunks);
+  sd.init(uint32_t(d_bytes), dchunks);
   float rsh = -INFINITY, rdel = 0.f;
-  auto load = [&](int t) {
-    const int r0 = t * kTile, rows = qrows - r0;
-    sq.load(rows, dchunks, [&](int r) {
-      const uint32_t tok = div_g(uint32_t(r0 + r), p);
-      return qp + int64_t(tok) * p.q_row + int64_t(uint32_t(r0 + r) - tok * uint32_t(p.G)) * p.q_head;
-    });
-    sd.load(rows, dchunks, [&](int r) {
-      const uint32_t tok = div_g(uint32_t(r0 + r), p);
-      return dp_ + (int64_t(tok) * p.hq + int64_t(uint32_t(r0 + r) - tok * uint32_t(p.G))) * p.d;
-    });
+  int g = t0 < t1 ? t0 / tiles : 0, tt = t0 < t1 ? t0 - g * tiles : 0;  // the step to load
+  auto load = [&]() {
+    const int64_t r0 = int64_t(tt) * TL::kRows;
+    const int rows = sg.other_len - tt * TL::kRows;
+    sq.load(qp + r0 * p.q_row + g * p.q_head, rows, q_bytes, head_bytes);
+    sd.load(dp_ + (r0 * p.hq + g) * p.d, rows, d_bytes, head_bytes);
     rsh = -INFINITY;
     rdel = 0.f;
-    if (lane < rows) {
-      const uint32_t tok = div_g(uint32_t(r0 + lane), p);
-      const int64_t at = int64_t(hk * p.G + int(uint32_t(r0 + lane) - tok * uint32_t(p.G))) * p.nq + sg.other + tok;
+    if (lane < rows && lane < TL::kRows) {
+      const int64_t at = int64_t(hk * p.G + g) * p.nq + sg.other + r0 + lane;
       const float lse = p.lse[at];
       rsh = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;
-      rdel = p.delta[at];
+      if (p.dk) rdel = p.delta[at];  // dV alone needs none, and none was formed
     }
+    if (++tt == tiles) tt = 0, ++g;
   };
-  if (t0 < t1) load(t0);
+  if (t0 < t1) load();
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1;
     sq.store(lq[buf]);
     sd.store(ld[buf]);
-    if (wave == 0) {
+    if (wave == 0 && lane < TL::kRows) {
       lsh[buf][lane] = rsh;
       ldel[buf][lane] = rdel;
     }
     __syncthreads();
-    if (t + 1 < t1) load(t + 1);
+    if (t + 1 < t1) load();
+    if (!busy) continue;
+    f32x16 s[TL::kGroups][KB], dp[TL::kGroups][KB];
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
-      f32x16 s{}, dp{};
+    for (int qb = 0; qb < TL::kGroups; ++qb) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b) s[qb][b] = dp[qb][b] = f32x16{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
-        s = E::mma(TL::rows(lq[buf], 32 * qb, f), kf[f], s);
-        dp = E::mma(TL::rows(ld[buf], 32 * qb, f), vf[f], dp);
-      }
+        const u32x4 a = TL::rows(lq[buf], 32 * qb, f), w = TL::rows(ld[buf], 32 * qb, f);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][32 * qb + 8 * g + 4 * half]);
-        const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][32 * qb + 8 * g + 4 * half]);
-        const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * g + j], c, sh[j]));
-          s[4 * g + j] = pr;
-          dp[4 * g + j] = pr * ((dp[4 * g + j] - de[j]) * dsmul);
-        }
-      }
-#pragma unroll
-      for (int st = 0; st < E::kSteps; ++st) {
-        const u32x4 pf = E::pack(s, st), sf = E::pack(dp, st);
-#pragma unroll
-        for (int d = 0; d < TL::kBlocks; ++d) {
-          dv[d] = E::mma(TL::cols(ld[buf], 32 * qb, st, d), pf, dv[d]);
-          dk[d] = E::mma(TL::cols(lq[buf], 32 * qb, st, d), sf, dk[d]);
+        for (int b = 0; b < KB; ++b) {
+          s[qb][b] = E::mma(a, kf[b][f], s[qb][b]);
+          dp[qb][b] = E::mma(w, vf[b][f], dp[qb][b]);
         }
       }
     }
-  }
-  if (!live) return;
-  // a masked key has no gradient, whatever its zeroed column collected
-  const float fk = on ? ldexpf(p.scale, -dse) : 0.f, fv = on ? ldexpf(1.f, -kPExp<T>) : 0.f;
-  if (!on)
 #pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) dk[d] = dv[d] = f32x16{};
-  const int64_t at = (row * p.hk + hk) * p.d, sp = int64_t(split) * p.nk * p.hk * p.d + at;
-  if (p.dk) store_cols<T, DP>(static_cast<T*>(p.dk) + at, p.nsplit > 1 ? p.part_a + sp : nullptr, dk, p.d, fk);
-  if (p.dv) store_cols<T, DP>(static_cast<T*>(p.dv) + at, p.nsplit > 1 ? p.part_b + sp : nullptr, dv, p.d, fv);
+    for (int qb = 0; qb < TL::kGroups; ++qb) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][32 * qb + 8 * i + 4 * half]);
+        const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][32 * qb + 8 * i + 4 * half]);
+        const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float pr = __builtin_amdgcn_exp2f(fmaf(s[qb][b][4 * i + j], c, sh[j]));
+            s[qb][b][4 * i + j] = pr;
+            dp[qb][b][4 * i + j] = pr * scaled<T>(dp[qb][b][4 * i + j] - de[j], dsmul);
+          }
+      }
+#pragma unroll
+      for (int st = 0; st < E::kSteps; ++st) {
+        u32x4 pf[KB], sf[KB];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) pf[b] = E::pack(s[qb][b], st), sf[b] = E::pack(dp[qb][b], st);
+#pragma unroll
+        for (int d = 0; d < TL::kBlocks; ++d) {
+          const u32x4 a = TL::cols(ld[buf], 32 * qb, st, d), w = TL::cols(lq[buf], 32 * qb, st, d);
+#pragma unroll
+          for (int b = 0; b < KB; ++b) {
+            dv[b][d] = E::mma(a, pf[b], dv[b][d]);
+            dk[b][d] = E::mma(w, sf[b], dk[b][d]);
+          }
+        }
+      }
+      }
+  }
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    if (!live[b]) continue;
+    // a masked key has no gradient, whatever its zeroed column collected
+    if (!on[b])
+#pragma unroll
+      for (int d = 0; d < TL::kBlocks; ++d) dk[b][d] = dv[b][d] = f32x16{};
+    const int64_t at = (row[b] * p.hk + hk) * p.d, sp = int64_t(split) * p.nk * p.hk * p.d + at;
+    if (p.dk) store_cols<T, DP>(static_cast<T*>(p.dk) + at, p.nsplit > 1 ? p.part_a + sp : nullptr, dk[b], p.d, ldexpf(p.scale, -dse));
+    if (p.dv) store_cols<T, DP>(static_cast<T*>(p.dv) + at, p.nsplit > 1 ? p.part_b + sp : nullptr, dv[b], p.d, ldexpf(1.f, -kPExp<T>));
+  }
 }
 
 // dst[i] = the sum of the splits' partial sums, in split order; four elements a thread
@@ -927,64 +1221,73 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float* part, int6
 
 // what the host decides before a launch
 struct FwdPlan {
-  int nw, qb, tiles, nsplit;
+  bool few;  // a sample's rows fit one tile of 32 columns (see fwd_kernel)
+  int tiles, nsplit;
 };
 struct BwdPlan {
-  int q_nw, q_qb, q_tiles, q_split;   // dQ
-  int k_nw, k_tiles, k_split;         // dK and dV
+  bool q_few;
+  int q_tiles, q_split;  // dQ
+  int k_tiles, k_split;  // dK and dV
+};
+
+// the backward pass's regions of the workspace
+struct BwdParts {
+  float *q_sum, *q_mean, *q_err, *k_sum, *v_sum;
+  uint32_t* bound;
 };
 
 // launches of one element type (defined once per type)
 template <typename T>
 int launch_fwd(const Params& p, const FwdPlan& f, hipStream_t s);
 template <typename T>
-int launch_bwd(Params p, const BwdPlan& b, float* part_q, float* part_k, float* part_v, uint32_t* bound, hipStream_t s);
+int launch_bwd(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s);
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 
-template <typename T, int DP, int NW, int QB>
+template <typename T, int DP, int NW, int QB, bool FEW>
 void launch_fwd_tile(const Params& p, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    fwd_kernel<T, DP, NW, QB, true><<<grid, NW * 64, 0, s>>>(p);
+    fwd_kernel<T, DP, NW, QB, true, FEW><<<grid, NW * 64, 0, s>>>(p);
   else
-    fwd_kernel<T, DP, NW, QB, false><<<grid, NW * 64, 0, s>>>(p);
+    fwd_kernel<T, DP, NW, QB, false, FEW><<<grid, NW * 64, 0, s>>>(p);
 }
 
 template <typename T, int DP>
 void launch_fwd_dim(const Params& p, const FwdPlan& f, hipStream_t s) {
-  if (f.nw == 1)
-    launch_fwd_tile<T, DP, 1, 1>(p, s);
+  if (f.few)
+    launch_fwd_tile<T, DP, 4, 1, true>(p, s);
   else
-    launch_fwd_tile<T, DP, 4, 1>(p, s);
+    launch_fwd_tile<T, DP, 4, tile_cfg(sizeof(T), DP).fwd_qb, false>(p, s);
 }
 
-template <typename T, int DP, int NW, int QB>
+template <typename T, int DP, int NW, int QB, bool FEW>
 void launch_dq_tile(const Params& p, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    dq_kernel<T, DP, NW, QB, true><<<grid, NW * 64, 0, s>>>(p);
+    dq_kernel<T, DP, NW, QB, true, FEW><<<grid, NW * 64, 0, s>>>(p);
   else
-    dq_kernel<T, DP, NW, QB, false><<<grid, NW * 64, 0, s>>>(p);
+    dq_kernel<T, DP, NW, QB, false, FEW><<<grid, NW * 64, 0, s>>>(p);
 }
 
 template <typename T, int DP>
 void launch_dq_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
-  if (b.q_nw == 1)
-    launch_dq_tile<T, DP, 1, 1>(p, s);
+  if (b.q_few)
+    launch_dq_tile<T, DP, 4, 1, true>(p, s);
   else
-    launch_dq_tile<T, DP, 4, 1>(p, s);
+    launch_dq_tile<T, DP, 4, tile_cfg(sizeof(T), DP).dq_qb, false>(p, s);
 }
 
 template <typename T, int DP>
-void launch_dkv_dim(const Params& p, hipStream_t s) {
+void launch_dkv_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
+  constexpr int KB = tile_cfg(sizeof(T), DP).dkv_kb;
   if (p.mask)
-    dkv_kernel<T, DP, 4, true><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, 4, KB, true><<<grid, 256, 0, s>>>(p);
   else
-    dkv_kernel<T, DP, 4, false><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, 4, KB, false><<<grid, 256, 0, s>>>(p);
 }
 
 template <typename T>
@@ -997,22 +1300,25 @@ int launch_fwd_impl(const Params& p, const FwdPlan& f, hipStream_t s) {
     launch_fwd_dim<T, 96>(p, f, s);
   else
     launch_fwd_dim<T, 128>(p, f, s);
-  if (p.nsplit > 1) fwd_join_kernel<T><<<unsigned((p.nq * p.hq + 3) / 4), 256, 0, s>>>(p);
+  if (p.nsplit > 1) fwd_join_kernel<T><<<unsigned(p.nq * p.hq), 256, 0, s>>>(p);
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;
 }
 
 template <typename T>
-int launch_bwd_impl(Params p, const BwdPlan& b, float* part_q, float* part_k, float* part_v, uint32_t* bound,
-                    hipStream_t s) {
-  const bool scaled = kPExp<T> != 0;
-  if (scaled) bound_clear_kernel<<<1, 64, 0, s>>>(bound);
-  p.bound = bound;
-  const int64_t groups = p.nq * p.hq + (scaled ? p.nk * p.hk : 0);
-  if (groups > 0) delta_kernel<T><<<unsigned((groups + 15) / 16), 256, 0, s>>>(p, scaled ? bound : nullptr);
-  if (p.dq && p.nq > 0) {
+int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s) {
+  p.bound = w.bound;
+  if constexpr (kPExp<T> != 0) {
+    const int64_t blocks = (p.nq * p.hq + p.nk * p.hk + 15) / 16;
+    bound_clear_kernel<<<1, 64, 0, s>>>(w.bound);
+    bound_kernel<T><<<unsigned(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(p, w.bound);
+  }
+  // dK reads the delta that the dQ pass forms, so that pass runs for either
+  if ((p.dq || p.dk) && p.nq > 0) {
     p.tiles = b.q_tiles;
     p.nsplit = b.q_split;
-    p.part_a = part_q;
+    p.part_a = w.q_sum;
+    p.part_b = w.q_mean;
+    p.part_e = w.q_err;
     if (p.d <= 32)
       launch_dq_dim<T, 32>(p, b, s);
     else if (p.d <= 64)
@@ -1021,29 +1327,26 @@ int launch_bwd_impl(Params p, const BwdPlan& b, float* part_q, float* part_k, fl
       launch_dq_dim<T, 96>(p, b, s);
     else
       launch_dq_dim<T, 128>(p, b, s);
-    if (p.nsplit > 1) {
-      const int64_t n4 = p.nq * p.hq * p.d / 4;
-      sum_splits_kernel<T><<<unsigned((n4 + 255) / 256), 256, 0, s>>>(part_q, n4, p.nsplit, static_cast<T*>(p.dq));
-    }
+    if (p.nsplit > 1) dq_join_kernel<T><<<unsigned(p.nq * p.hq), 256, 0, s>>>(p);
   }
   if ((p.dk || p.dv) && p.nk > 0) {
     p.tiles = b.k_tiles;
     p.nsplit = b.k_split;
-    p.part_a = part_k;
-    p.part_b = part_v;
+    p.part_a = w.k_sum;
+    p.part_b = w.v_sum;
     if (p.d <= 32)
-      launch_dkv_dim<T, 32>(p, s);
+      launch_dkv_dim<T, 32>(p, b, s);
     else if (p.d <= 64)
-      launch_dkv_dim<T, 64>(p, s);
+      launch_dkv_dim<T, 64>(p, b, s);
     else if (p.d <= 96)
-      launch_dkv_dim<T, 96>(p, s);
+      launch_dkv_dim<T, 96>(p, b, s);
     else
-      launch_dkv_dim<T, 128>(p, s);
+      launch_dkv_dim<T, 128>(p, b, s);
     if (p.nsplit > 1) {
       const int64_t n4 = p.nk * p.hk * p.d / 4;
       const unsigned grid = unsigned((n4 + 255) / 256);
-      if (p.dk) sum_splits_kernel<T><<<grid, 256, 0, s>>>(part_k, n4, p.nsplit, static_cast<T*>(p.dk));
-      if (p.dv) sum_splits_kernel<T><<<grid, 256, 0, s>>>(part_v, n4, p.nsplit, static_cast<T*>(p.dv));
+      if (p.dk) sum_splits_kernel<T><<<grid, 256, 0, s>>>(w.k_sum, n4, p.nsplit, static_cast<T*>(p.dk));
+      if (p.dv) sum_splits_kernel<T><<<grid, 256, 0, s>>>(w.v_sum, n4, p.nsplit, static_cast<T*>(p.dv));
     }
   }
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;

@@ -12,58 +12,69 @@ int launch_fwd<_Float16>(const Params&, const FwdPlan&, hipStream_t);
 template <>
 int launch_fwd<__bf16>(const Params&, const FwdPlan&, hipStream_t);
 template <>
-int launch_bwd<float>(Params, const BwdPlan&, float*, float*, float*, uint32_t*, hipStream_t);
+int launch_bwd<float>(Params, const BwdPlan&, const BwdParts&, hipStream_t);
 template <>
-int launch_bwd<_Float16>(Params, const BwdPlan&, float*, float*, float*, uint32_t*, hipStream_t);
+int launch_bwd<_Float16>(Params, const BwdPlan&, const BwdParts&, hipStream_t);
 template <>
-int launch_bwd<__bf16>(Params, const BwdPlan&, float*, float*, float*, uint32_t*, hipStream_t);
+int launch_bwd<__bf16>(Params, const BwdPlan&, const BwdParts&, hipStream_t);
 
 namespace {
 
+int esize(int32_t dtype) { return dtype == SSC_F32 ? 4 : 2; }
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// splits so that about `target` workgroups run, each of at least `least` streamed tiles
-int pick_split(int64_t wgs, int64_t target, int64_t stream_tiles, int64_t least) {
+constexpr int64_t kSlots = 512;  // workgroups the chip holds at once: 256 CUs, two each
+
+// Splits of the streamed axis so that the chip is full, each of at least `least` tiles: with fewer workgroups than
+// slots, as many as fill them; with up to a few rounds of them, enough that the last round's idle slots matter little
+// (`rounds` > 0; the partial sums of more splits cost little next to that).
+int pick_split(int64_t wgs, int64_t stream_tiles, int64_t least, int64_t rounds) {
   if (wgs < 1) wgs = 1;
-  int64_t n = target / wgs;
+  int64_t n = wgs >= rounds * kSlots ? 1 : (rounds * kSlots + wgs - 1) / wgs;
   const int64_t most = stream_tiles / least;
   if (n > most) n = most;
-  if (n > 128) n = 128;
+  if (n > kMaxSplit) n = kMaxSplit;
   return n < 1 ? 1 : int(n);
+}
+
+Cfg cfg_of(const ssc_attn_shape& a) {
+  return tile_cfg(esize(a.dtype), a.head_dim <= 32 ? 32 : a.head_dim <= 64 ? 64 : a.head_dim <= 96 ? 96 : 128);
+}
+
+// workgroups of a pass: its tiles (an average over the samples) and heads
+int64_t busy_wgs(int64_t rows, int64_t cols, const ssc_attn_shape& a) {
+  const int64_t tiles = ceil_div(rows, cols);
+  return (tiles > a.batch ? tiles : a.batch) * a.heads_kv;
 }
 
 FwdPlan fwd_plan(const ssc_attn_shape& a) {
   const int64_t rows = a.nq * (a.heads_q / a.heads_kv);
-  const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), kTile);
+  const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype)));
   FwdPlan f{};
-  // one wave a tile where a sample's rows fit 32 columns: the keys are then split over many more workgroups
-  f.nw = rows <= 32 * int64_t(a.batch) ? 1 : 4;
-  f.qb = 1;
-  const int64_t cols = f.nw * f.qb * 32;
+  f.few = rows <= 32 * int64_t(a.batch);
+  const int64_t cols = f.few ? 32 : 4 * 32 * cfg_of(a).fwd_qb;
   f.tiles = int(rows / cols + a.batch + 2);
-  const int64_t busy = (rows / cols > a.batch ? rows / cols : a.batch) * a.heads_kv;
-  f.nsplit = pick_split(busy, f.nw == 1 ? 1280 : 512, kv_tiles, 2);
+  // few rows: each of a workgroup's four waves gets tiles of its own, at least four
+  f.nsplit = pick_split(busy_wgs(rows, cols, a), kv_tiles, f.few ? 16 : 4, 1);
   return f;
 }
 
 BwdPlan bwd_plan(const ssc_attn_shape& a) {
   const int64_t rows = a.nq * (a.heads_q / a.heads_kv);
-  const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), kTile), q_tiles = ceil_div(ceil_div(rows, a.batch), kTile);
+  const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype))), q_tiles = ceil_div(ceil_div(rows, a.batch), tile_rows(esize(a.dtype)));
   BwdPlan b{};
-  b.q_nw = rows <= 32 * int64_t(a.batch) ? 1 : 4;
-  b.q_qb = 1;
-  const int64_t qc = b.q_nw * b.q_qb * 32, kc = 128;
+  b.q_few = rows <= 32 * int64_t(a.batch);
+  const int64_t qc = b.q_few ? 32 : 4 * 32 * cfg_of(a).dq_qb, kc = 4 * 32 * cfg_of(a).dkv_kb;
   b.q_tiles = int(rows / qc + a.batch + 2);
   b.k_tiles = int(a.nk / kc + a.batch + 2);
-  const int64_t qbusy = (rows / qc > a.batch ? rows / qc : a.batch) * a.heads_kv;
-  const int64_t kbusy = (a.nk / kc > a.batch ? a.nk / kc : a.batch) * a.heads_kv;
-  b.q_split = pick_split(qbusy, b.q_nw == 1 ? 1280 : 512, kv_tiles, 2);
-  b.k_split = pick_split(kbusy, 512, q_tiles, 2);
+  b.q_split = pick_split(busy_wgs(rows, qc, a), kv_tiles, b.q_few ? 16 : 4, 1);
+  b.k_split = pick_split(busy_wgs(a.nk, kc, a), q_tiles, 8, 4);
   return b;
 }
 
 struct Ws {
-  size_t part_q = 0, part_k = 0, part_v = 0, delta = 0, bound = 0, total = 0;
+  size_t part_q = 0, mean_q = 0, err_q = 0, part_k = 0, part_v = 0, delta = 0, bound = 0, total = 0;
 };
 
 Ws ws_layout(const ssc_attn_shape& a, bool backward) {
@@ -85,7 +96,13 @@ Ws ws_layout(const ssc_attn_shape& a, bool backward) {
     const BwdPlan b = bwd_plan(a);
     w.bound = take(256);
     w.delta = take(qn * 4);
-    if (b.q_split > 1) w.part_q = take(size_t(b.q_split) * qn * d * 4);
+    if (b.q_split > 1) {
+      w.part_q = take(size_t(b.q_split) * qn * d * 4);
+      if (a.dtype != SSC_F32) {
+        w.mean_q = take(size_t(b.q_split) * qn * d * 4);
+        w.err_q = take(size_t(b.q_split) * qn * 4);
+      }
+    }
     if (b.k_split > 1) {
       w.part_k = take(size_t(b.k_split) * kn * d * 4);
       w.part_v = take(size_t(b.k_split) * kn * d * 4);
@@ -94,8 +111,6 @@ Ws ws_layout(const ssc_attn_shape& a, bool backward) {
   w.total = off < 256 ? 256 : off;
   return w;
 }
-
-int esize(int32_t dtype) { return dtype == SSC_F32 ? 4 : 2; }
 
 int check_shape(const ssc_attn_shape* a) {
   if (!a) return SSC_ERR_INVALID_ARG;
@@ -110,9 +125,11 @@ int check_shape(const ssc_attn_shape* a) {
   if (a->nq * (a->heads_q / a->heads_kv) > (1LL << 30)) return SSC_ERR_UNSUPPORTED;
   const float s = a->scale;
   if (!(s - s == 0.f)) return SSC_ERR_INVALID_ARG;  // infinite or NaN
-  const int64_t st[6] = {a->q_row_stride, a->q_head_stride, a->k_row_stride, a->k_head_stride, a->v_row_stride,
-                         a->v_head_stride};
-  for (int64_t v : st)
+  const int64_t rows[3] = {a->q_row_stride, a->k_row_stride, a->v_row_stride};
+  const int64_t heads[3] = {a->q_head_stride, a->k_head_stride, a->v_head_stride};
+  for (int64_t v : rows)
+    if (v < 0 || v > SSC_MAX_ATTN_ROW_STRIDE || (v * e) % 16 != 0) return SSC_ERR_INVALID_ARG;
+  for (int64_t v : heads)
     if (v < 0 || v > (1LL << 40) || (v * e) % 16 != 0) return SSC_ERR_INVALID_ARG;
   const FwdPlan f = fwd_plan(*a);
   const BwdPlan b = bwd_plan(*a);
@@ -226,13 +243,12 @@ extern "C" int ssc_cross_attn_bwd(const ssc_attn_shape* shape, const void* q, co
   p.qoff = q_offsets;
   p.koff = kv_offsets;
   p.mask = kv_mask;
-  float* pq = reinterpret_cast<float*>(ws + w.part_q);
-  float* pk = reinterpret_cast<float*>(ws + w.part_k);
-  float* pv = reinterpret_cast<float*>(ws + w.part_v);
-  uint32_t* bound = reinterpret_cast<uint32_t*>(ws + w.bound);
+  const BwdParts parts{reinterpret_cast<float*>(ws + w.part_q), reinterpret_cast<float*>(ws + w.mean_q),
+                       reinterpret_cast<float*>(ws + w.err_q),  reinterpret_cast<float*>(ws + w.part_k),
+                       reinterpret_cast<float*>(ws + w.part_v), reinterpret_cast<uint32_t*>(ws + w.bound)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (a.dtype == SSC_F32) return launch_bwd<float>(p, b, pq, pk, pv, bound, s);
-  if (a.dtype == SSC_F16) return launch_bwd<_Float16>(p, b, pq, pk, pv, bound, s);
-  return launch_bwd<__bf16>(p, b, pq, pk, pv, bound, s);
+  if (a.dtype == SSC_F32) return launch_bwd<float>(p, b, parts, s);
+  if (a.dtype == SSC_F16) return launch_bwd<_Float16>(p, b, parts, s);
+  return launch_bwd<__bf16>(p, b, parts, s);
 }

@@ -9,9 +9,8 @@ int launch_fwd<_Float16>(const Params& p, const FwdPlan& f, hipStream_t s) {
   return launch_fwd_impl<_Float16>(p, f, s);
 }
 template <>
-int launch_bwd<_Float16>(Params p, const BwdPlan& b, float* part_q, float* part_k, float* part_v, uint32_t* bound,
-                    hipStream_t s) {
-  return launch_bwd_impl<_Float16>(p, b, part_q, part_k, part_v, bound, s);
+int launch_bwd<_Float16>(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s) {
+  return launch_bwd_impl<_Float16>(p, b, w, s);
 }
 
 }  // namespace attn
