@@ -171,6 +171,8 @@ struct TileOf {
   static constexpr int kFrags = DP / (2 * kVec);   // operand fragments along the head dimension
   static constexpr int kBlocks = DP / 32;          // 32-wide blocks of the head dimension
 
+  // whether fragment f lies past the head's `dchunks` chunks; 16-bit products are too short to gain from a branch
+  __device__ static __forceinline__ bool skip(int f, int dchunks) { return sizeof(T) == 4 && 2 * f >= dchunks; }
   // rows r0 .. r0+31 as MFMA rows, reduction indices of fragment f (chunk 2f + lane/32)
   __device__ static __forceinline__ u32x4 rows(const char* tile, int r0, int f) {
     const int lane = threadIdx.x & 63;
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
       for (int b = 0; b < QB; ++b) s[b][kb] = f32x16{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
+        if (TL::skip(f, dchunks)) break;
         const u32x4 a = TL::rows(lk, 32 * kb, f);
 #pragma unroll
         for (int b = 0; b < QB; ++b) s[b][kb] = E::mma(a, qf[b][f], s[b][kb]);
@@ -888,6 +891,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
       for (int b = 0; b < QB; ++b) s[b] = dp[b] = f32x16{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
+        if (TL::skip(f, dchunks)) break;
         const u32x4 a = TL::rows(lk, 32 * kb, f), v = TL::rows(lv, 32 * kb, f);
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
@@ -1145,6 +1149,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
       for (int b = 0; b < KB; ++b) s[qb][b] = dp[qb][b] = f32x16{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
+        if (TL::skip(f, dchunks)) break;
         const u32x4 a = TL::rows(lq[buf], 32 * qb, f), w = TL::rows(ld[buf], 32 * qb, f);
 #pragma unroll
         for (int b = 0; b < KB; ++b) {

@@ -24,14 +24,13 @@ int esize(int32_t dtype) { return dtype == SSC_F32 ? 4 : 2; }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int64_t kSlots = 512;  // workgroups the chip holds at once: 256 CUs, two each
+constexpr int64_t kCUs = 256;
 
-// Splits of the streamed axis so that the chip is full, each of at least `least` tiles: with fewer workgroups than
-// slots, as many as fill them; with up to a few rounds of them, enough that the last round's idle slots matter little
-// (`rounds` > 0; the partial sums of more splits cost little next to that).
-int pick_split(int64_t wgs, int64_t stream_tiles, int64_t least, int64_t rounds) {
+// Splits of the streamed axis where the workgroups of the rows alone do not fill the chip: about `want` workgroups,
+// each of at least `least` tiles.
+int pick_split(int64_t wgs, int64_t want, int64_t stream_tiles, int64_t least) {
   if (wgs < 1) wgs = 1;
-  int64_t n = wgs >= rounds * kSlots ? 1 : (rounds * kSlots + wgs - 1) / wgs;
+  int64_t n = want / wgs;
   const int64_t most = stream_tiles / least;
   if (n > most) n = most;
   if (n > kMaxSplit) n = kMaxSplit;
@@ -48,6 +47,15 @@ int64_t busy_wgs(int64_t rows, int64_t cols, const ssc_attn_shape& a) {
   return (tiles > a.batch ? tiles : a.batch) * a.heads_kv;
 }
 
+// Splits of the forward and dQ passes.  Rows: two workgroups a CU fill the chip; a split is worth its share of the join
+// from four 16-bit tiles on, and from one fp32 tile, whose products take about eight times as long.  Few rows: as
+// many workgroups as fit at once by their LDS, a whole number of times the rows', each wave with two tiles or more.
+int row_split(bool few, int64_t wgs, int64_t kv_tiles, const ssc_attn_shape& a) {
+  const int e = esize(a.dtype);
+  if (few) return pick_split(wgs, a.head_dim <= 64 ? 2 * kCUs : kCUs, kv_tiles, 8);
+  return wgs >= kCUs ? 1 : pick_split(wgs, 2 * kCUs, kv_tiles, e == 4 ? 1 : 4);
+}
+
 FwdPlan fwd_plan(const ssc_attn_shape& a) {
   const int64_t rows = a.nq * (a.heads_q / a.heads_kv);
   const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype)));
@@ -55,21 +63,24 @@ FwdPlan fwd_plan(const ssc_attn_shape& a) {
   f.few = rows <= 32 * int64_t(a.batch);
   const int64_t cols = f.few ? 32 : 4 * 32 * cfg_of(a).fwd_qb;
   f.tiles = int(rows / cols + a.batch + 2);
-  // few rows: each of a workgroup's four waves gets tiles of its own, at least four
-  f.nsplit = pick_split(busy_wgs(rows, cols, a), kv_tiles, f.few ? 16 : 4, 1);
+  f.nsplit = row_split(f.few, busy_wgs(rows, cols, a), kv_tiles, a);
   return f;
 }
 
 BwdPlan bwd_plan(const ssc_attn_shape& a) {
   const int64_t rows = a.nq * (a.heads_q / a.heads_kv);
-  const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype))), q_tiles = ceil_div(ceil_div(rows, a.batch), tile_rows(esize(a.dtype)));
+  const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype)));
+  const int64_t q_tiles = ceil_div(ceil_div(rows, a.batch), tile_rows(esize(a.dtype)));
   BwdPlan b{};
   b.q_few = rows <= 32 * int64_t(a.batch);
   const int64_t qc = b.q_few ? 32 : 4 * 32 * cfg_of(a).dq_qb, kc = 4 * 32 * cfg_of(a).dkv_kb;
   b.q_tiles = int(rows / qc + a.batch + 2);
   b.k_tiles = int(a.nk / kc + a.batch + 2);
-  b.q_split = pick_split(busy_wgs(rows, qc, a), kv_tiles, b.q_few ? 16 : 4, 1);
-  b.k_split = pick_split(busy_wgs(a.nk, kc, a), q_tiles, 8, 4);
+  b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a);
+  // dK and dV of short encoder sequences: few column tiles over long streams, split into several rounds of workgroups
+  // so that the last round's idle CUs and the samples' different lengths matter little
+  const int64_t wgs = busy_wgs(a.nk, kc, a);
+  b.k_split = wgs >= 4 * 2 * kCUs ? 1 : pick_split(wgs, 4 * 2 * kCUs, q_tiles, a.dtype == SSC_F32 ? 1 : 8);
   return b;
 }
 

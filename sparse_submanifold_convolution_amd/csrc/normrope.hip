@@ -98,7 +98,13 @@ __device__ __forceinline__ void angles(const RopeParams& p, int64_t row, int sub
       a = a < 0 ? 0 : (a < p.axes ? a : p.axes - 1);
       double t = double(p.pos[row * p.pos_row + a]) * p.turns[pair];
       t -= rint(t);
-      sincospif(2.f * float(t), &si[j], &co[j]);
+      if constexpr (sizeof(T) == 4) {
+        sincospif(2.f * float(t), &si[j], &co[j]);
+      } else {
+        // the hardware's sine and cosine take revolutions; their error is far below a 16-bit result's rounding
+        si[j] = __builtin_amdgcn_sinf(float(t));
+        co[j] = __builtin_amdgcn_cosf(float(t));
+      }
     }
   }
 }
@@ -203,29 +209,48 @@ __global__ void __launch_bounds__(256) rope_bwd(RopeParams p) {
     if (NORM && w && h < heads && mine)
       Vec<T>::unpack(*reinterpret_cast<const u32x4*>(w + (p.per_head ? hh * p.d : 0) + sub * N), wf[i]);
   }
+  // a head past the last reads the last's rows and writes nothing; so does one whose output gradient is not given
+  const T *src[kRopeHeads], *up[kRopeHeads];
+  T* out[kRopeHeads];
+  int64_t srow[kRopeHeads], urow[kRopeHeads];
+  bool on[kRopeHeads];
+#pragma unroll
+  for (int i = 0; i < kRopeHeads; ++i) {
+    const int h = h0 + i < heads ? h0 + i : heads - 1;
+    const bool isq = h < p.hq;
+    const int hh = isq ? h : h - p.hq;
+    const T* u = static_cast<const T*>(isq ? p.dqo : p.dko);
+    T* o = static_cast<T*>(isq ? p.qo : p.ko);
+    on[i] = h0 + i < heads && u;
+    src[i] = (isq ? static_cast<const T*>(p.q) + hh * p.q_head : static_cast<const T*>(p.k) + hh * p.k_head) + sub * N;
+    srow[i] = isq ? p.q_row : p.k_row;
+    up[i] = u + hh * p.d + sub * N;
+    urow[i] = int64_t(isq ? p.hq : p.hk) * p.d;
+    out[i] = o ? o + hh * p.d + sub * N : nullptr;
+  }
   for (int64_t row = int64_t(blockIdx.x) * GPB + grp; row < p.n; row += int64_t(gridDim.x) * GPB) {
+    // all of the row's loads are on their way before the angles are formed
+    u32x4 gv[kRopeHeads], xv[kRopeHeads];
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) {
+      gv[i] = xv[i] = u32x4{0, 0, 0, 0};
+      if (mine && on[i]) {
+        gv[i] = *reinterpret_cast<const u32x4*>(up[i] + row * urow[i]);
+        if constexpr (NORM) xv[i] = *reinterpret_cast<const u32x4*>(src[i] + row * srow[i]);
+      }
+    }
     float co[NA], si[NA];
 #pragma unroll
     for (int j = 0; j < NA; ++j) co[j] = 1.f, si[j] = 0.f;
     if (p.pairs > 0) angles<T, HALVES, NA>(p, row, sub, co, si);
 #pragma unroll
     for (int i = 0; i < kRopeHeads; ++i) {
-      const int h = h0 + i;
-      if (h >= heads) continue;
-      const bool isq = h < p.hq;
-      const int hh = isq ? h : h - p.hq;
-      void* out = isq ? p.qo : p.ko;
-      const T* up = static_cast<const T*>(isq ? p.dqo : p.dko);
-      if (!up) continue;
-      const int64_t at = isq ? (row * p.hq + hh) * p.d : (row * p.hk + hh) * p.d;
       float g[N];
-      Vec<T>::unpack(mine ? *reinterpret_cast<const u32x4*>(up + at + sub * N) : u32x4{0, 0, 0, 0}, g);
+      Vec<T>::unpack(gv[i], g);
       if (p.pairs > 0) turn<HALVES, true>(g, co, si, p.pairs, sub);
       if constexpr (NORM) {
-        const T* src = isq ? static_cast<const T*>(p.q) + row * p.q_row + hh * p.q_head
-                           : static_cast<const T*>(p.k) + row * p.k_row + hh * p.k_head;
         float x[N];
-        Vec<T>::unpack(mine ? *reinterpret_cast<const u32x4*>(src + sub * N) : u32x4{0, 0, 0, 0}, x);
+        Vec<T>::unpack(xv[i], x);
         float sq = 0.f, dot = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -238,11 +263,11 @@ __global__ void __launch_bounds__(256) rope_bwd(RopeParams p) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const float xn = x[j] * r;
-          if constexpr (DW) acc[i][j] = fmaf(g[j], xn, acc[i][j]);
+          if constexpr (DW) acc[i][j] = fmaf(g[j], on[i] ? xn : 0.f, acc[i][j]);
           g[j] = r * (g[j] * wf[i][j] - xn * s);
         }
       }
-      if (mine && out) *reinterpret_cast<u32x4*>(static_cast<T*>(out) + at + sub * N) = Vec<T>::pack(g);
+      if (mine && on[i] && out[i]) *reinterpret_cast<u32x4*>(out[i] + row * urow[i]) = Vec<T>::pack(g);
     }
   }
   if constexpr (DW) {
@@ -267,25 +292,28 @@ __global__ void __launch_bounds__(256) rope_bwd(RopeParams p) {
   }
 }
 
-// dw[c] = the partial sums of column c over the blocks (and, for one weight shared by all heads, over the heads).
-// A block of 256 = 16 columns x 16 partial rows.
+// The weight gradients: column c's partial sums over the row blocks (and, for one weight shared by all heads, over the
+// heads), queries' columns first, then the keys'.  A workgroup is 16 columns x 16 shares of the partial rows.
 template <typename T>
-__global__ void __launch_bounds__(256) rope_dw(const float* part, int nparts, int heads_all, int h0, int heads, int d,
-                                               int per_head, T* dw) {
-  const int c = blockIdx.x * 16 + threadIdx.x % 16, ph = threadIdx.x / 16;
-  const int cols = per_head ? heads * d : d;
+__global__ void __launch_bounds__(256) rope_dw(const float* part, int nparts, int hq, int hk, int d, int per_head, T* dqw,
+                                               T* dkw) {
+  const int qcols = dqw ? (per_head ? hq * d : d) : 0, kcols = dkw ? (per_head ? hk * d : d) : 0;
+  int c = blockIdx.x * 16 + threadIdx.x % 16;
+  const int ph = threadIdx.x / 16;
+  const bool isq = c < qcols;
+  T* dw = isq ? dqw : dkw;
+  if (!isq) c -= qcols;
+  const bool any = isq || c < kcols;
   float v = 0.f;
-  if (c < cols) {
-    const int reps = per_head ? 1 : heads;
-    for (int64_t t = ph; t < int64_t(nparts) * reps; t += 16) {
-      const int64_t b = t / reps, hr = t - b * reps;
-      v += part[(b * heads_all + h0 + hr) * d + c];
-    }
+  if (any) {
+    const int reps = per_head ? 1 : (isq ? hq : hk), h0 = isq ? 0 : hq;
+    for (int64_t b = ph; b < nparts; b += 16)
+      for (int r = 0; r < reps; ++r) v += part[(b * (hq + hk) + h0 + r) * d + c];
   }
   __shared__ float red[16][17];
   red[ph][threadIdx.x % 16] = v;
   __syncthreads();
-  if (ph == 0 && c < cols) {
+  if (ph == 0 && any) {
     float s = 0.f;
     for (int i = 0; i < 16; ++i) s += red[i][threadIdx.x];
     dw[c] = T(s);
@@ -409,15 +437,10 @@ void rope_dispatch(const ssc_norm_rope_shape& a, RopeParams& p, bool back, bool 
 
 template <typename T>
 void launch_dw(const ssc_norm_rope_shape& a, const float* part, void* dqw, void* dkw, hipStream_t s) {
-  const int heads = a.heads_q + a.heads_kv, nparts = int(row_blocks(a));
-  auto one = [&](void* dw, int h0, int h) {
-    if (!dw || h < 1) return;
-    const int cols = (a.weight_per_head ? h : 1) * a.head_dim;
-    rope_dw<T><<<unsigned((cols + 15) / 16), 256, 0, s>>>(part, nparts, heads, h0, h, a.head_dim, a.weight_per_head,
-                                                          static_cast<T*>(dw));
-  };
-  one(dqw, 0, a.heads_q);
-  one(dkw, a.heads_q, a.heads_kv);
+  const int per = a.weight_per_head ? a.head_dim : 0;
+  const int cols = (dqw ? (per ? a.heads_q * per : a.head_dim) : 0) + (dkw ? (per ? a.heads_kv * per : a.head_dim) : 0);
+  rope_dw<T><<<unsigned((cols + 15) / 16), 256, 0, s>>>(part, int(row_blocks(a)), a.heads_q, a.heads_kv, a.head_dim,
+                                                        a.weight_per_head, static_cast<T*>(dqw), static_cast<T*>(dkw));
 }
 
 }  // namespace
