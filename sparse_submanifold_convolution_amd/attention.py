@@ -251,10 +251,18 @@ def _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale):
     return _AttnShape(nq, nk, qr, qh, kr, kh, vr, vh, batch, hq, hk, dim, DTYPE_CODE[dt], float(scale)), dev, dt
 
 
+_unused: dict[int, torch.Tensor] = {}  # by device: stands for the workspace of calls that use none
+
+
 def _attn_workspace(sh: _AttnShape, backward: int, dev: torch.device) -> torch.Tensor:
     nbytes = int(lib().ssc_cross_attn_workspace_bytes(ctypes.byref(sh), backward))
     if nbytes == 0:
         raise SSCError("ssc_cross_attn_workspace_bytes", 2)
+    if nbytes == 256 and not backward:  # the smallest size: nothing is kept there
+        ws = _unused.get(dev.index)
+        if ws is None:
+            ws = _unused[dev.index] = torch.empty(256, dtype=torch.uint8, device=dev)
+        return ws
     return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 

@@ -162,11 +162,11 @@ __device__ __forceinline__ s16x4 lds_tr16(const void* p) {
 }
 
 // Geometry of one LDS tile of kRows streamed rows and DP (head size rounded up to 32) elements, and its reads
-template <typename T, int DP>
+template <typename T, int DP, int R = tile_rows(sizeof(T))>
 struct TileOf {
   static constexpr int kVec = Elt<T>::kVec;
   static constexpr int CPR = DP / kVec;            // chunks per row
-  static constexpr int kRows = tile_rows(sizeof(T)), kGroups = kRows / 32;
+  static constexpr int kRows = R, kGroups = R / 32;
   static constexpr int kBytes = kRows * CPR * 16;
   static constexpr int kFrags = DP / (2 * kVec);   // operand fragments along the head dimension
   static constexpr int kBlocks = DP / 32;          // 32-wide blocks of the head dimension
@@ -208,12 +208,34 @@ struct TileOf {
   }
 };
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, int(bytes), 0x00027000);
+}
+
+// Tiles of R rows, one after another: where the next one starts and how many bytes its rows span (row strides are
+// bounded so that a whole tile's fit 32 bits)
+template <int R>
+struct Walk {
+  const char* at;
+  int64_t step;
+  uint32_t row_bytes, head_bytes, full;
+  __device__ __forceinline__ void init(int64_t row, uint32_t head) {
+    row_bytes = uint32_t(row);
+    head_bytes = head;
+    full = uint32_t(R - 1) * row_bytes + head;
+    step = R * row;
+  }
+  __device__ __forceinline__ uint32_t span(int rows) const {
+    return rows >= R ? full : uint32_t(rows - 1) * row_bytes + head_bytes;
+  }
+};
+
 // A tile on its way from memory to LDS, NT threads (a workgroup, or one wave): 16-byte chunks in registers.  The loads go through a buffer
 // descriptor that ends with the sample's last row, so rows past it (and chunks past the head) read as zeros with no
 // branch, and a thread's offsets inside a tile are computed once for all tiles.
-template <typename T, int DP, int NT>
+template <typename T, int DP, int NT, int R = tile_rows(sizeof(T))>
 struct Stage {
-  using TL = TileOf<T, DP>;
+  using TL = TileOf<T, DP, R>;
   static constexpr int kTotal = TL::kRows * TL::CPR;
   static constexpr int N = (kTotal + NT - 1) / NT;
   u32x4 r[N];
@@ -228,11 +250,9 @@ struct Stage {
       off[i] = (any(i) && c < dchunks) ? uint32_t(row) * row_bytes + uint32_t(c) * 16u : 0xFFFFFFF0u;
     }
   }
-  // the tile at `base`, of whose rows `rows` (> 0) exist, each of head_bytes
-  __device__ __forceinline__ void load(const void* base, int rows, int64_t row_bytes, uint32_t head_bytes) {
-    const int64_t span = int64_t(rows - 1) * row_bytes + head_bytes;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
-                                                        int(span < 0xFFFFFFE0ll ? uint32_t(span) : 0xFFFFFFE0u), 0x00027000);
+  // the rows at `base` that the next `span` bytes hold
+  __device__ __forceinline__ void load(const void* base, uint32_t span) {
+    const auto rsrc = buffer_of(base, span);
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, int(off[i]), 0, 0));
   }
@@ -272,46 +292,39 @@ struct Segment {
   int32_t tile;    // tile number inside the segment
 };
 
-// Finds tile t of the concatenated segments, each holding ceil(len * mult / cols) tiles; false past the last.
+// Finds tile t of the concatenated segments, each holding ceil(len * mult / cols) tiles; false past the last.  Each
+// lane looks at one segment; all offsets are loaded side by side.
 __device__ __forceinline__ bool find_segment(const int32_t* off, int64_t n, const int32_t* other_off, int64_t other_n,
                                              int batch, int mult, int cols, int t, Segment* seg) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
   for (int base = 0; base < batch + 2; base += 64) {
     const int s = base + lane;
-    int64_t b = 0, e = 0;
-    if (s < batch + 2) {
-      b = s == 0 ? 0 : clamp_off(off, s - 1, n);
-      e = s == batch + 1 ? n : clamp_off(off, s, n);
-      if (e < b) e = b;
-    }
-    int incl = int(((e - b) * mult + cols - 1) / cols);
-    const int mine = incl;
+    const int lo = s < 1 ? 0 : (s - 1 < batch ? s - 1 : batch), hi = s < batch ? s : batch;
+    int64_t b = clamp_off(off, lo, n), e = clamp_off(off, hi, n);
+    const int64_t ob = clamp_off(other_off, lo, other_n), oe = clamp_off(other_off, hi, other_n);
+    if (s == 0) b = 0;
+    if (s == batch + 1) e = n;
+    if (e < b || s > batch + 1) e = b;
+    const int len = int(e - b), olen = s >= 1 && s <= batch && oe > ob ? int(oe - ob) : 0;
+    const int mine = int((int64_t(len) * mult + cols - 1) / cols);
+    int incl = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(incl, d);
       if (lane >= d) incl += o;
     }
     const int total = uniform(__shfl(incl, 63));
-    if (t - before < total) {
-      const uint64_t past = __ballot(incl > t - before);
-      const int w = uniform(__ffsll((unsigned long long)past) - 1);
-      const int sw = uniform(base + w);
-      const int64_t bw = sw == 0 ? 0 : clamp_off(off, sw - 1, n);
-      const int64_t ew = sw == batch + 1 ? n : clamp_off(off, sw, n);
-      seg->begin = uniform(bw);
-      seg->len = uniform(int(ew > bw ? ew - bw : 0));
-      seg->tile = uniform(t - before - __shfl(incl - mine, w));
-      seg->other = 0;
-      seg->other_len = 0;
-      if (sw >= 1 && sw <= batch) {
-        const int64_t ob = clamp_off(other_off, sw - 1, other_n), oe = clamp_off(other_off, sw, other_n);
-        seg->other = uniform(ob);
-        seg->other_len = uniform(int(oe > ob ? oe - ob : 0));
-      }
+    if (t < total) {
+      const int w = uniform(__ffsll((unsigned long long)__ballot(incl > t)) - 1);
+      // rows are below 2^28: offsets fit an int
+      seg->begin = __builtin_amdgcn_readlane(int(b), w);
+      seg->len = __builtin_amdgcn_readlane(len, w);
+      seg->tile = t - __builtin_amdgcn_readlane(incl - mine, w);
+      seg->other = __builtin_amdgcn_readlane(int(ob), w);
+      seg->other_len = __builtin_amdgcn_readlane(olen, w);
       return true;
     }
-    before += total;
+    t -= total;
   }
   return false;
 }
@@ -452,21 +465,25 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
   split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
   constexpr int step = FEW ? NW : 1;
   if (FEW) t0 += wave;
-  const T* kp = static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head;
-  const T* vp = static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head;
   const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
+  Walk<TL::kRows> wk, wv;
+  wk.init(p.k_row * int64_t(sizeof(T)), head_bytes);
+  wv.init(p.v_row * int64_t(sizeof(T)), head_bytes);
+  wk.at = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head) + t0 * wk.step;
+  wv.at = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head) + t0 * wv.step;
   Stage<T, DP, NT> sk, sv;
-  sk.init(uint32_t(p.k_row * int64_t(sizeof(T))), dchunks);
-  sv.init(uint32_t(p.v_row * int64_t(sizeof(T))), dchunks);
+  sk.init(wk.row_bytes, dchunks);
+  sv.init(wv.row_bytes, dchunks);
   uint8_t keep[Stage<T, DP, NT>::N];
   bool kept = false;  // the key of streamed row `lane`
   auto load = [&](int t) {
-    const int64_t k0 = int64_t(t) * TL::kRows;
     const int rows = sg.other_len - t * TL::kRows;
-    sk.load(kp + k0 * p.k_row, rows, p.k_row * int64_t(sizeof(T)), head_bytes);
-    sv.load(vp + k0 * p.v_row, rows, p.v_row * int64_t(sizeof(T)), head_bytes);
+    sk.load(wk.at, wk.span(rows));
+    sv.load(wv.at, wv.span(rows));
+    wk.at += step * wk.step;
+    wv.at += step * wv.step;
     if constexpr (MASK) {
-      const uint8_t* mp = p.mask + sg.other + k0;
+      const uint8_t* mp = p.mask + sg.other + int64_t(t) * TL::kRows;
 #pragma unroll
       for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
         const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
@@ -654,17 +671,21 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
 
 constexpr int kMaxSplit = 128;
 
-// Joins the splits of the forward pass: a workgroup per (row, head).  The splits' weights are formed once, side by
-// side; the four waves then add their splits' rows and the wave sums are added in order.
-template <typename T>
+// up to this many splits a wave joins a row's one after another, four rows a workgroup
+constexpr int kFewSplits = 8;
+
+// Joins the splits of the forward pass.  Many splits (WIDE): a workgroup per (row, head), the weights formed side by
+// side, the four waves adding their splits' rows and the wave sums added in order.  Few: a wave per (row, head).
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
-  __shared__ float lw[kMaxSplit], lsum[4][SSC_MAX_HEAD_DIM];
+  __shared__ float lw[4][WIDE ? kMaxSplit : 64], lsum[WIDE ? 4 : 1][SSC_MAX_HEAD_DIM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t rh = blockIdx.x, n = p.nq * p.hq;
-  // every wave forms the same maximum and sum
-  float mx = -INFINITY, ms[kMaxSplit / 64], ls[kMaxSplit / 64];
+  constexpr int M = WIDE ? kMaxSplit / 64 : 1;
+  const int64_t n = p.nq * p.hq, rh = WIDE ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 4 + wave;
+  if (!WIDE && rh >= n) return;
+  float mx = -INFINITY, ms[M], ls[M];
 #pragma unroll
-  for (int i = 0; i < kMaxSplit / 64; ++i) {
+  for (int i = 0; i < M; ++i) {
     const int s = lane + 64 * i;
     ms[i] = s < p.nsplit ? p.part_b[2 * (s * n + rh)] : -INFINITY;
     ls[i] = s < p.nsplit ? p.part_b[2 * (s * n + rh) + 1] : 0.f;
@@ -674,30 +695,38 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
   for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
   float total = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxSplit / 64; ++i) {
+  for (int i = 0; i < M; ++i) {
     const float w = ms[i] == mx ? 1.f : __builtin_amdgcn_exp2f(ms[i] - mx);
     total += w * ls[i];
-    if (wave == 0) lw[lane + 64 * i] = w;
+    lw[wave][lane + 64 * i] = w;
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-  __syncthreads();
+  const bool some = total != 0.f;
+  const float inv = some ? 1.f / total : 0.f;
+  wave_fence();
   float acc[2] = {0.f, 0.f};
 #pragma unroll 4
-  for (int s = wave; s < p.nsplit; s += 4) {
-    const float w = lw[s];
+  for (int s = WIDE ? wave : 0; s < p.nsplit; s += WIDE ? 4 : 1) {
+    const float w = lw[wave][s];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (lane + 64 * e < p.d) acc[e] = fmaf(w, p.part_a[(s * n + rh) * p.d + lane + 64 * e], acc[e]);
   }
+  T* op = static_cast<T*>(p.o) + rh * p.d;
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) lsum[wave][lane + 64 * e] = acc[e];
-  __syncthreads();
-  const bool some = total != 0.f;
-  const float inv = some ? 1.f / total : 0.f;
-  const int e = threadIdx.x;
-  if (e < p.d) static_cast<T*>(p.o)[rh * p.d + e] = T(((lsum[0][e] + lsum[1][e]) + (lsum[2][e] + lsum[3][e])) * inv);
-  if (e == 0) p.lse[(rh % p.hq) * p.nq + rh / p.hq] = some ? (mx - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+    for (int e = 0; e < 2; ++e) lsum[wave][lane + 64 * e] = acc[e];
+    __syncthreads();
+    const int e = threadIdx.x;
+    if (e < p.d) op[e] = T(((lsum[0][e] + lsum[1][e]) + (lsum[2][e] + lsum[3][e])) * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 64 * e < p.d) op[lane + 64 * e] = T(acc[e] * inv);
+  }
+  if (lane == 0 && (!WIDE || wave == 0))
+    p.lse[(rh % p.hq) * p.nq + rh / p.hq] = some ? (mx - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -834,21 +863,25 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
   split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
   constexpr int step = FEW ? NW : 1;
   if (FEW) t0 += wave;
-  const T* kp = static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head;
-  const T* vp = static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head;
   const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
+  Walk<TL::kRows> wk, wv;
+  wk.init(p.k_row * int64_t(sizeof(T)), head_bytes);
+  wv.init(p.v_row * int64_t(sizeof(T)), head_bytes);
+  wk.at = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head) + t0 * wk.step;
+  wv.at = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head) + t0 * wv.step;
   Stage<T, DP, NT> sk, sv;
-  sk.init(uint32_t(p.k_row * int64_t(sizeof(T))), dchunks);
-  sv.init(uint32_t(p.v_row * int64_t(sizeof(T))), dchunks);
+  sk.init(wk.row_bytes, dchunks);
+  sv.init(wv.row_bytes, dchunks);
   uint8_t keep[Stage<T, DP, NT>::N];
   bool kept = false;
   auto load = [&](int t) {
-    const int64_t k0 = int64_t(t) * TL::kRows;
     const int rows = sg.other_len - t * TL::kRows;
-    sk.load(kp + k0 * p.k_row, rows, p.k_row * int64_t(sizeof(T)), head_bytes);
-    sv.load(vp + k0 * p.v_row, rows, p.v_row * int64_t(sizeof(T)), head_bytes);
+    sk.load(wk.at, wk.span(rows));
+    sv.load(wv.at, wv.span(rows));
+    wk.at += step * wk.step;
+    wv.at += step * wv.step;
     if constexpr (MASK) {
-      const uint8_t* mp = p.mask + sg.other + k0;
+      const uint8_t* mp = p.mask + sg.other + int64_t(t) * TL::kRows;
 #pragma unroll
       for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
         const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
@@ -1029,13 +1062,13 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
   }
 }
 
-// Joins the splits of dQ: a workgroup per (row, head), its waves taking the splits in turn.  e is the sum of the
-// splits' sums of dS (see dq_kernel).
-template <typename T>
+// Joins the splits of dQ, in the two forms of the forward join.  e is the sum of the splits' sums of dS (see dq_kernel).
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
-  __shared__ float la[4][SSC_MAX_HEAD_DIM], lm[4][SSC_MAX_HEAD_DIM];
+  __shared__ float la[WIDE ? 4 : 1][SSC_MAX_HEAD_DIM], lm[WIDE ? 4 : 1][SSC_MAX_HEAD_DIM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t rh = blockIdx.x, n = p.nq * p.hq;
+  const int64_t n = p.nq * p.hq, rh = WIDE ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 4 + wave;
+  if (!WIDE && rh >= n) return;
   float e = 0.f;
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -1043,174 +1076,226 @@ __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
       if (lane + 64 * i < p.nsplit) e += p.part_e[(lane + 64 * i) * n + rh];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) e += __shfl_xor(e, d);
-    if (threadIdx.x == 0) p.delta[(rh % p.hq) * p.nq + rh / p.hq] += e;
+    if (lane == 0 && (!WIDE || wave == 0)) p.delta[(rh % p.hq) * p.nq + rh / p.hq] += e;
   }
   if (!p.dq) return;
   float a[2] = {0.f, 0.f}, m[2] = {0.f, 0.f};
 #pragma unroll 4
-  for (int s = wave; s < p.nsplit; s += 4)
+  for (int s = WIDE ? wave : 0; s < p.nsplit; s += WIDE ? 4 : 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (lane + 64 * i < p.d) {
         a[i] += p.part_a[(s * n + rh) * p.d + lane + 64 * i];
         if constexpr (sizeof(T) == 2) m[i] += p.part_b[(s * n + rh) * p.d + lane + 64 * i];
       }
+  T* op = static_cast<T*>(p.dq) + rh * p.d;
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) la[wave][lane + 64 * i] = a[i], lm[wave][lane + 64 * i] = m[i];
-  __syncthreads();
-  const int i = threadIdx.x;
-  if (i < p.d) {
-    const float as = (la[0][i] + la[1][i]) + (la[2][i] + la[3][i]), mm = (lm[0][i] + lm[1][i]) + (lm[2][i] + lm[3][i]);
-    static_cast<T*>(p.dq)[rh * p.d + i] = T(fmaf(-e, mm, as));
+    for (int i = 0; i < 2; ++i) la[wave][lane + 64 * i] = a[i], lm[wave][lane + 64 * i] = m[i];
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < p.d) {
+      const float as = (la[0][i] + la[1][i]) + (la[2][i] + la[3][i]), mm = (lm[0][i] + lm[1][i]) + (lm[2][i] + lm[3][i]);
+      op[i] = T(fmaf(-e, mm, as));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 64 * i < p.d) op[lane + 64 * i] = T(fmaf(-e, m[i], a[i]));
   }
 }
 
-template <typename T, int DP, int NW, int KB, bool MASK>
+// dK and dV of 32 key columns a wave, over 32-row blocks of queries.  The blocks are software pipelined: while block i's
+// probabilities and dS are formed on the vector units, the matrix units work on block i + 1's scores and on block
+// i - 1's products with dout and q, whose operands do not depend on them.  Four LDS tiles in turn let one barrier a
+// block suffice: the tile written for block i + 1 was last read for block i - 3.
+template <typename T, int DP, int NW, bool MASK>
 __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
-  using TL = TileOf<T, DP>;
+  constexpr int R = 32;
+  using TL = TileOf<T, DP, R>;
   using E = Elt<T>;
-  constexpr int NT = NW * 64, TC = NW * KB * 32;
-  __shared__ __align__(16) char lq[2][TL::kBytes];
-  __shared__ __align__(16) char ld[2][TL::kBytes];
-  __shared__ __align__(16) float lsh[2][TL::kRows], ldel[2][TL::kRows];
+  constexpr int NT = NW * 64, TC = NW * 32, KS = E::kSteps;
+  __shared__ __align__(16) char lds[4][2 * TL::kBytes];
+  __shared__ __align__(16) float lsh[4][R], ldel[4][R];
   const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
   if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
   const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
   Segment sg;
   if (!find_segment(p.koff, p.nk, p.qoff, p.nq, p.batch, 1, TC, tile, &sg)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
   const int dchunks = p.d / TL::kVec;
   const float c = p.scale * kLog2e;
   const int dse = ds_exp<T>(p);
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);
 
-  bool live[KB], on[KB];
-  int64_t row[KB];
-  u32x4 kf[KB][TL::kFrags], vf[KB][TL::kFrags];
-  f32x16 dk[KB][TL::kBlocks], dv[KB][TL::kBlocks];
+  const int col = sg.tile * TC + wave * 32 + (lane & 31);
+  const bool live = col < sg.len;
+  const int64_t row = sg.begin + (live ? col : 0);
+  const bool on = live && (!MASK || p.mask[row] != 0);
+  u32x4 kf[TL::kFrags], vf[TL::kFrags];
+  load_cols<T, DP>(static_cast<const T*>(p.k) + row * p.k_row + hk * p.k_head, on, dchunks, kf);
+  load_cols<T, DP>(static_cast<const T*>(p.v) + row * p.v_row + hk * p.v_head, on, dchunks, vf);
+  f32x16 dk[TL::kBlocks], dv[TL::kBlocks];
 #pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    const int col = sg.tile * TC + (wave * KB + b) * 32 + (lane & 31);
-    live[b] = col < sg.len;
-    row[b] = sg.begin + (live[b] ? col : 0);
-    on[b] = live[b] && (!MASK || p.mask[row[b]] != 0);
-    load_cols<T, DP>(static_cast<const T*>(p.k) + row[b] * p.k_row + hk * p.k_head, on[b], dchunks, kf[b]);
-    load_cols<T, DP>(static_cast<const T*>(p.v) + row[b] * p.v_row + hk * p.v_head, on[b], dchunks, vf[b]);
-#pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) dk[b][d] = dv[b][d] = f32x16{};
-  }
+  for (int d = 0; d < TL::kBlocks; ++d) dk[d] = dv[d] = f32x16{};
   // waves whose columns all lie past the sample's keys only help to stage
-  const bool busy = sg.tile * TC + wave * KB * 32 < sg.len;
+  const bool busy = sg.tile * TC + wave * 32 < sg.len;
 
-  // the sample's queries, head after head of the group: step t is head t / tiles, tile t % tiles
-  const int tiles = (sg.other_len + TL::kRows - 1) / TL::kRows;
-  int t0, t1;
-  split_range(tiles * p.G, split, p.nsplit, &t0, &t1);
-  const T* qp = static_cast<const T*>(p.q) + sg.other * p.q_row + int64_t(hk) * p.G * p.q_head;
-  const T* dp_ = static_cast<const T*>(p.dout) + (sg.other * p.hq + int64_t(hk) * p.G) * p.d;
+  // the sample's queries, head after head of the group: block n is head n / blocks, rows 32 (n mod blocks) ..
+  const int blocks = (sg.other_len + R - 1) / R;
+  int n0, n1;
+  split_range(blocks * p.G, split, p.nsplit, &n0, &n1);
   const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
-  const int64_t q_bytes = p.q_row * int64_t(sizeof(T)), d_bytes = int64_t(p.hq) * head_bytes;
-  Stage<T, DP, NT> sq, sd;
-  sq.init(uint32_t(q_bytes), dchunks);
-  sd.init(uint32_t(d_bytes), dchunks);
-  float rsh = -INFINITY, rdel = 0.f;
-  int g = t0 < t1 ? t0 / tiles : 0, tt = t0 < t1 ? t0 - g * tiles : 0;  // the step to load
-  auto load = [&]() {
-    const int64_t r0 = int64_t(tt) * TL::kRows;
-    const int rows = sg.other_len - tt * TL::kRows;
-    sq.load(qp + r0 * p.q_row + g * p.q_head, rows, q_bytes, head_bytes);
-    sd.load(dp_ + (r0 * p.hq + g) * p.d, rows, d_bytes, head_bytes);
-    rsh = -INFINITY;
-    rdel = 0.f;
-    if (lane < rows && lane < TL::kRows) {
-      const int64_t at = int64_t(hk * p.G + g) * p.nq + sg.other + r0 + lane;
-      const float lse = p.lse[at];
-      rsh = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;
-      if (p.dk) rdel = p.delta[at];  // dV alone needs none, and none was formed
-    }
-    if (++tt == tiles) tt = 0, ++g;
+  Walk<R> wq, wd;
+  wq.init(p.q_row * int64_t(sizeof(T)), head_bytes);
+  wd.init(int64_t(p.hq) * head_bytes, head_bytes);
+  Stage<T, DP, NT, R> sq, sd;
+  sq.init(wq.row_bytes, dchunks);
+  sd.init(wd.row_bytes, dchunks);
+  const float *lse_at = nullptr, *del_at = nullptr;
+  int g = n0 < n1 ? n0 / blocks : 0, left = n0 < n1 ? sg.other_len - (n0 - g * blocks) * R : 0;  // rows of head g to load
+  auto seek = [&]() {
+    const int64_t r0 = sg.other + (sg.other_len - left), head = hk * p.G + g;
+    wq.at = reinterpret_cast<const char*>(static_cast<const T*>(p.q) + r0 * p.q_row + head * p.q_head);
+    wd.at = reinterpret_cast<const char*>(static_cast<const T*>(p.dout) + (r0 * p.hq + head) * p.d);
+    lse_at = p.lse + head * p.nq + r0;
+    del_at = p.delta + head * p.nq + r0;
   };
-  if (t0 < t1) load();
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    sq.store(lq[buf]);
-    sd.store(ld[buf]);
-    if (wave == 0 && lane < TL::kRows) {
-      lsh[buf][lane] = rsh;
+  float rlse = 0.f, rdel = 0.f;
+  int rows = 0;  // of the block on its way
+  const uint32_t lane_off = wave == 0 && lane < R ? lane * 4 : 0xFFFFFFF0u;
+  auto load = [&]() {
+    sq.load(wq.at, wq.span(left));
+    sd.load(wd.at, wd.span(left));
+    const uint32_t bytes = uint32_t(left < R ? left : R) * 4;
+    rlse = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_of(lse_at, bytes), int(lane_off), 0, 0));
+    // dV alone needs no delta, and none was formed
+    if (p.dk) rdel = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_of(del_at, bytes), int(lane_off), 0, 0));
+    rows = left;
+    left -= R;
+    wq.at += wq.step;
+    wd.at += wd.step;
+    lse_at += R;
+    del_at += R;
+    if (left <= 0) {
+      left = sg.other_len;
+      ++g;
+      seek();
+    }
+  };
+  auto store = [&](int buf) {
+    sq.store(lds[buf]);
+    sd.store(lds[buf] + TL::kBytes);
+    if (wave == 0 && lane < R) {
+      // rows past the sample and rows with no key: weights 0
+      lsh[buf][lane] = lane >= rows || rlse == -INFINITY ? -INFINITY : float(kPExp<T>) - rlse * kLog2e;
       ldel[buf][lane] = rdel;
     }
-    __syncthreads();
-    if (t + 1 < t1) load();
-    if (!busy) continue;
-    f32x16 s[TL::kGroups][KB], dp[TL::kGroups][KB];
+  };
+  auto scores = [&](int buf, f32x16& s, f32x16& dp) {
+    const char* tq = lds[buf];
+    const char* td = tq + TL::kBytes;
+    s = dp = f32x16{};
 #pragma unroll
-    for (int qb = 0; qb < TL::kGroups; ++qb) {
+    for (int f = 0; f < TL::kFrags; ++f) {
+      if (TL::skip(f, dchunks)) break;
+      s = E::mma(TL::rows(tq, 0, f), kf[f], s);
+      dp = E::mma(TL::rows(td, 0, f), vf[f], dp);
+    }
+  };
+  auto products = [&](int buf, const u32x4 (&pf)[KS], const u32x4 (&sf)[KS]) {
+    const char* tq = lds[buf];
+    const char* td = tq + TL::kBytes;
 #pragma unroll
-      for (int b = 0; b < KB; ++b) s[qb][b] = dp[qb][b] = f32x16{};
+    for (int st = 0; st < KS; ++st)
 #pragma unroll
-      for (int f = 0; f < TL::kFrags; ++f) {
-        if (TL::skip(f, dchunks)) break;
-        const u32x4 a = TL::rows(lq[buf], 32 * qb, f), w = TL::rows(ld[buf], 32 * qb, f);
+      for (int d = 0; d < TL::kBlocks; ++d) {
+        dv[d] = E::mma(TL::cols(td, 0, st, d), pf[st], dv[d]);
+        dk[d] = E::mma(TL::cols(tq, 0, st, d), sf[st], dk[d]);
+      }
+  };
+  auto weights = [&](int buf, f32x16& s, f32x16& dp, u32x4 (&pf)[KS], u32x4 (&sf)[KS]) {
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          s[qb][b] = E::mma(a, kf[b][f], s[qb][b]);
-          dp[qb][b] = E::mma(w, vf[b][f], dp[qb][b]);
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][8 * i + 4 * half]);
+      const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][8 * i + 4 * half]);
+      const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * i + j], c, sh[j]));
+        s[4 * i + j] = pr;
+        dp[4 * i + j] = pr * scaled<T>(dp[4 * i + j] - de[j], dsmul);
       }
     }
 #pragma unroll
-    for (int qb = 0; qb < TL::kGroups; ++qb) {
+    for (int st = 0; st < KS; ++st) pf[st] = E::pack(s, st), sf[st] = E::pack(dp, st);
+  };
+
+  f32x16 s[2], dp[2];
+  u32x4 pf[2][KS], sf[2][KS];
+  const int n = n1 - n0;
+  if (n > 0) {
+    seek();
+    load();
+    // block -1: no weights, and a tile of zeros to multiply them with
+    for (int i = threadIdx.x; i < 2 * TL::kBytes / 16; i += NT) reinterpret_cast<u32x4*>(lds[3])[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][32 * qb + 8 * i + 4 * half]);
-        const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][32 * qb + 8 * i + 4 * half]);
-        const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float pr = __builtin_amdgcn_exp2f(fmaf(s[qb][b][4 * i + j], c, sh[j]));
-            s[qb][b][4 * i + j] = pr;
-            dp[qb][b][4 * i + j] = pr * scaled<T>(dp[qb][b][4 * i + j] - de[j], dsmul);
-          }
-      }
-#pragma unroll
-      for (int st = 0; st < E::kSteps; ++st) {
-        u32x4 pf[KB], sf[KB];
-#pragma unroll
-        for (int b = 0; b < KB; ++b) pf[b] = E::pack(s[qb][b], st), sf[b] = E::pack(dp[qb][b], st);
-#pragma unroll
-        for (int d = 0; d < TL::kBlocks; ++d) {
-          const u32x4 a = TL::cols(ld[buf], 32 * qb, st, d), w = TL::cols(lq[buf], 32 * qb, st, d);
-#pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            dv[b][d] = E::mma(a, pf[b], dv[b][d]);
-            dk[b][d] = E::mma(w, sf[b], dk[b][d]);
-          }
-        }
-      }
-      }
+    for (int st = 0; st < KS; ++st) pf[1][st] = sf[1][st] = u32x4{0, 0, 0, 0};
+    store(0);
+    if (n > 1) load();
+    __syncthreads();
   }
-#pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    if (!live[b]) continue;
-    // a masked key has no gradient, whatever its zeroed column collected
-    if (!on[b])
-#pragma unroll
-      for (int d = 0; d < TL::kBlocks; ++d) dk[b][d] = dv[b][d] = f32x16{};
-    const int64_t at = (row[b] * p.hk + hk) * p.d, sp = int64_t(split) * p.nk * p.hk * p.d + at;
-    if (p.dk) store_cols<T, DP>(static_cast<T*>(p.dk) + at, p.nsplit > 1 ? p.part_a + sp : nullptr, dk[b], p.d, ldexpf(p.scale, -dse));
-    if (p.dv) store_cols<T, DP>(static_cast<T*>(p.dv) + at, p.nsplit > 1 ? p.part_b + sp : nullptr, dv[b], p.d, ldexpf(1.f, -kPExp<T>));
+  auto stage = [&](int i) {
+    store((i + 1) & 3);  // past the last block: rows of a block before, whose scores nothing uses
+    __syncthreads();
+    if (i + 2 < n) load();
+  };
+  if (!busy) {
+    for (int i = 0; i < n; ++i) stage(i);
+    return;
   }
+  if (n > 0) {
+    scores(0, s[0], dp[0]);
+    auto step = [&](int i, f32x16& sc, f32x16& dc, f32x16& sn, f32x16& dn, u32x4 (&pc)[KS], u32x4 (&fc)[KS],
+                    u32x4 (&pp)[KS], u32x4 (&fp)[KS]) {
+      stage(i);
+      scores((i + 1) & 3, sn, dn);
+      products((i + 3) & 3, pp, fp);
+      weights(i & 3, sc, dc, pc, fc);
+    };
+    int i = 0;
+    for (; i + 1 < n; i += 2) {
+      step(i, s[0], dp[0], s[1], dp[1], pf[0], sf[0], pf[1], sf[1]);
+      step(i + 1, s[1], dp[1], s[0], dp[0], pf[1], sf[1], pf[0], sf[0]);
+    }
+    if (i < n) {
+      step(i, s[0], dp[0], s[1], dp[1], pf[0], sf[0], pf[1], sf[1]);
+      products(i & 3, pf[0], sf[0]);
+    } else {
+      products((n - 1) & 3, pf[1], sf[1]);
+    }
+  }
+
+  if (!live) return;
+  // a masked key has no gradient, whatever its zeroed column collected
+  if (!on)
+#pragma unroll
+    for (int d = 0; d < TL::kBlocks; ++d) dk[d] = dv[d] = f32x16{};
+  const int64_t o = (row * p.hk + hk) * p.d, sp = int64_t(split) * p.nk * p.hk * p.d + o;
+  if (p.dk) store_cols<T, DP>(static_cast<T*>(p.dk) + o, p.nsplit > 1 ? p.part_a + sp : nullptr, dk, p.d, ldexpf(p.scale, -dse));
+  if (p.dv) store_cols<T, DP>(static_cast<T*>(p.dv) + o, p.nsplit > 1 ? p.part_b + sp : nullptr, dv, p.d, ldexpf(1.f, -kPExp<T>));
 }
 
-// dst[i] = the sum of the splits' partial sums, in split order; four elements a thread
+// dK (blockIdx.y 0) and dV (1): the splits' partial sums added in split order; four elements a thread
 template <typename T>
-__global__ void __launch_bounds__(256) sum_splits_kernel(const float* part, int64_t n4, int nsplit, T* dst) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const float4* src = reinterpret_cast<const float4*>(part);
+__global__ void __launch_bounds__(64) sum_splits_kernel(const float* part_k, const float* part_v, int64_t n4, int nsplit,
+                                                        T* dk, T* dv) {
+  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
+  T* dst = blockIdx.y ? dv : dk;
+  if (i >= n4 || !dst) return;
+  const float4* src = reinterpret_cast<const float4*>(blockIdx.y ? part_v : part_k);
   float4 a = src[i];
+#pragma unroll 8
   for (int s = 1; s < nsplit; ++s) {
     const float4 b = src[int64_t(s) * n4 + i];
     a.x += b.x;
@@ -1288,11 +1373,26 @@ void launch_dq_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
 template <typename T, int DP>
 void launch_dkv_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
-  constexpr int KB = tile_cfg(sizeof(T), DP).dkv_kb;
   if (p.mask)
-    dkv_kernel<T, DP, 4, KB, true><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, 4, true><<<grid, 256, 0, s>>>(p);
   else
-    dkv_kernel<T, DP, 4, KB, false><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, 4, false><<<grid, 256, 0, s>>>(p);
+}
+
+template <typename T>
+void launch_fwd_join(const Params& p, hipStream_t s) {
+  if (p.nsplit > kFewSplits)
+    fwd_join_kernel<T, true><<<unsigned(p.nq * p.hq), 256, 0, s>>>(p);
+  else
+    fwd_join_kernel<T, false><<<unsigned((p.nq * p.hq + 3) / 4), 256, 0, s>>>(p);
+}
+
+template <typename T>
+void launch_dq_join(const Params& p, hipStream_t s) {
+  if (p.nsplit > kFewSplits)
+    dq_join_kernel<T, true><<<unsigned(p.nq * p.hq), 256, 0, s>>>(p);
+  else
+    dq_join_kernel<T, false><<<unsigned((p.nq * p.hq + 3) / 4), 256, 0, s>>>(p);
 }
 
 template <typename T>
@@ -1305,7 +1405,7 @@ int launch_fwd_impl(const Params& p, const FwdPlan& f, hipStream_t s) {
     launch_fwd_dim<T, 96>(p, f, s);
   else
     launch_fwd_dim<T, 128>(p, f, s);
-  if (p.nsplit > 1) fwd_join_kernel<T><<<unsigned(p.nq * p.hq), 256, 0, s>>>(p);
+  if (p.nsplit > 1) launch_fwd_join<T>(p, s);
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;
 }
 
@@ -1332,7 +1432,7 @@ int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s
       launch_dq_dim<T, 96>(p, b, s);
     else
       launch_dq_dim<T, 128>(p, b, s);
-    if (p.nsplit > 1) dq_join_kernel<T><<<unsigned(p.nq * p.hq), 256, 0, s>>>(p);
+    if (p.nsplit > 1) launch_dq_join<T>(p, s);
   }
   if ((p.dk || p.dv) && p.nk > 0) {
     p.tiles = b.k_tiles;
@@ -1349,9 +1449,8 @@ int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s
       launch_dkv_dim<T, 128>(p, b, s);
     if (p.nsplit > 1) {
       const int64_t n4 = p.nk * p.hk * p.d / 4;
-      const unsigned grid = unsigned((n4 + 255) / 256);
-      if (p.dk) sum_splits_kernel<T><<<grid, 256, 0, s>>>(w.k_sum, n4, p.nsplit, static_cast<T*>(p.dk));
-      if (p.dv) sum_splits_kernel<T><<<grid, 256, 0, s>>>(w.v_sum, n4, p.nsplit, static_cast<T*>(p.dv));
+      sum_splits_kernel<T><<<dim3(unsigned((n4 + 63) / 64), 2), 64, 0, s>>>(w.k_sum, w.v_sum, n4, p.nsplit,
+                                                                            static_cast<T*>(p.dk), static_cast<T*>(p.dv));
     }
   }
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;

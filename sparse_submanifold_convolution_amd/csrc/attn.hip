@@ -78,9 +78,10 @@ BwdPlan bwd_plan(const ssc_attn_shape& a) {
   b.k_tiles = int(a.nk / kc + a.batch + 2);
   b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a);
   // dK and dV of short encoder sequences: few column tiles over long streams, split into several rounds of workgroups
-  // so that the last round's idle CUs and the samples' different lengths matter little
-  const int64_t wgs = busy_wgs(a.nk, kc, a);
-  b.k_split = wgs >= 4 * 2 * kCUs ? 1 : pick_split(wgs, 4 * 2 * kCUs, q_tiles, a.dtype == SSC_F32 ? 1 : 8);
+  // so that the last round's idle CUs and the samples' different lengths matter little.  fp32's blocks are so long
+  // that one workgroup a CU does.
+  const int64_t wgs = busy_wgs(a.nk, kc, a), want = a.dtype == SSC_F32 ? kCUs : 4 * 2 * kCUs;
+  b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? 4 : 8);
   return b;
 }
 
