@@ -53,7 +53,7 @@ struct Params {
   int32_t gshift;      // r / G = (r * gmul) >> gshift for r < 2^31
   float scale;
   int32_t tiles, nsplit;
-  // splits: partial sums [nsplit][rows][d]; forward part_b: [nsplit][rows][2] (max, sum); dQ part_e: [nsplit][rows]
+  // splits: partial sums [nsplit][rows][d]; forward part_b: [nsplit][rows][2] (max, sum); dQ part_e: [nsplit][rows][2]
   float *part_a, *part_b, *part_e;
 };
 
@@ -96,6 +96,10 @@ struct Elt<_Float16> {
   __device__ static __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
   }
+  // acc + the two elements a word holds
+  __device__ static __forceinline__ float sum(uint32_t a, float acc) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), f16x2{_Float16(1.f), _Float16(1.f)}, acc, false);
+  }
   __device__ static __forceinline__ float dot(uint32_t a, uint32_t b, float acc) {
     return fmaf(hi(a), hi(b), fmaf(lo(a), lo(b), acc));
   }
@@ -122,6 +126,10 @@ struct Elt<__bf16> {
   }
   __device__ static __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  }
+  // acc + the two elements a word holds
+  __device__ static __forceinline__ float sum(uint32_t a, float acc) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), bf16x2{__bf16(1.f), __bf16(1.f)}, acc, false);
   }
   __device__ static __forceinline__ float dot(uint32_t a, uint32_t b, float acc) {
     return fmaf(hi(a), hi(b), fmaf(lo(a), lo(b), acc));
@@ -795,17 +803,19 @@ __device__ __forceinline__ int ds_exp(const Params& p) {
   }
 }
 
-// v times dS's power of two, which only fp16 has
+// dP - delta times dS's power of two, which only fp16 has; `ndel` is -delta times it already
 template <typename T>
-__device__ __forceinline__ float scaled(float v, float mul) {
-  return kPExp<T> == 0 ? v : v * mul;
+__device__ __forceinline__ float less_delta(float dp, float ndel, float mul) {
+  return kPExp<T> == 0 ? dp + ndel : fmaf(dp, mul, ndel);
 }
 
 // dQ, and the exact delta.  The forward result that delta = dout . out is formed from was rounded to 16 bits, and that
 // error meets every key of the row with one sign: where attention is peaked it outweighs dS itself.  The sum of a row's
-// dS is zero, so the sum e of the dS formed with the rounded delta is the error: delta + e is exact to fp32, and
-// dq = scale (sum dS k - e sum P k).  The second sum is one more product on operands that are at hand; the dK pass
-// reads the corrected delta.  fp32 results need none of it.
+// dS is zero, so the sum e of the dS formed with the rounded delta is the error, and dq = scale (sum dS k - e sum P k).
+// With the sum of the values of dS as they are rounded for the product in e's place, their rounding goes out along the
+// keys' mean as well (the error of dq against 64 bits fell from twice that of a result only rounded at the end to 1.4
+// times).  The second sum is one more product on operands that are at hand; the dK pass reads delta + e.  fp32 needs
+// none of it.
 template <typename T, int DP, int NW, int QB, bool MASK, bool FEW>
 __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
   using TL = TileOf<T, DP>;
@@ -814,7 +824,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
   constexpr bool kFix = sizeof(T) == 2;
   __shared__ __align__(16) char lds[2 * BUFS * TL::kBytes];
   __shared__ unsigned long long lvalid[BUFS];
-  __shared__ float le[FEW ? (NW + 1) * 32 : 1];  // the waves' sums of dS, then delta
+  __shared__ float le[FEW ? (2 * NW + 1) * 32 : 1];  // the waves' sums of dS, of its rounded values, then delta
   const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
   if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
   const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
@@ -830,7 +840,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
   int head[QB];
   bool live[QB];
   u32x4 qf[QB][TL::kFrags], df[QB][TL::kFrags];
-  float sh[QB], del[QB], esum[QB];
+  float sh[QB], del[QB], ndel[QB], esum[QB], rsum[QB];
   f32x16 acc[QB][TL::kBlocks], mean[kFix ? QB : 1][TL::kBlocks];
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
@@ -849,9 +859,10 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
 #pragma unroll
       for (int e = 0; e < 4; ++e) dot = E::dot(df[b][f][e], of[f][e], dot);
     del[b] = dot + half_swap(dot);
+    ndel[b] = -del[b] * dsmul;
     const float lse = live[b] ? p.lse[int64_t(head[b]) * p.nq + row[b]] : -INFINITY;
     sh[b] = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;  // rows with no key: probabilities 0
-    esum[b] = 0.f;
+    esum[b] = rsum[b] = 0.f;
 #pragma unroll
     for (int d = 0; d < TL::kBlocks; ++d) {
       acc[b][d] = f32x16{};
@@ -949,7 +960,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
       for (int b = 0; b < QB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          dp[b][r] = s[b][r] * scaled<T>(dp[b][r] - del[b], dsmul);
+          dp[b][r] = s[b][r] * less_delta<T>(dp[b][r], ndel[b], dsmul);
           if constexpr (kFix) esum[b] += dp[b][r];
         }
 #pragma unroll
@@ -958,7 +969,11 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
           sf[b] = E::pack(dp[b], st);
-          if constexpr (kFix) pf[b] = E::pack(s[b], st);
+          if constexpr (kFix) {
+            pf[b] = E::pack(s[b], st);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rsum[b] = E::sum(sf[b][j], rsum[b]);
+          }
         }
 #pragma unroll
         for (int d = 0; d < TL::kBlocks; ++d) {
@@ -972,16 +987,17 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
       }
     }
   }
-  // dS carries 2^dse and P 2^kPExp: e in units of delta is esum 2^-dse
+  // dS carries 2^dse and P 2^kPExp: the sums in units of delta are esum 2^-dse and rsum 2^-dse
   const float f = ldexpf(p.scale, -dse), unit = ldexpf(1.f, -dse), punit = ldexpf(1.f, dse - kPExp<T>);
   if constexpr (FEW) {
     // the waves' sums, added in wave order; 2 NW threads share a column's elements
     float* all = reinterpret_cast<float*>(lds);
     float* mine = all + wave * DP * 33;
-    const float e = kFix ? esum[0] + half_swap(esum[0]) : 0.f;
+    const float e = kFix ? esum[0] + half_swap(esum[0]) : 0.f, re = kFix ? rsum[0] + half_swap(rsum[0]) : 0.f;
     if (half == 0) {
       le[wave * 32 + lane] = e;
-      if (wave == 0) le[NW * 32 + lane] = del[0];
+      le[(NW + wave) * 32 + lane] = re;
+      if (wave == 0) le[2 * NW * 32 + lane] = del[0];
     }
     constexpr int TPC = 2 * NW;
     const int col = threadIdx.x / TPC, e0 = threadIdx.x % TPC;
@@ -992,7 +1008,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
     const int ohead = hk * p.G + int(r - tok * uint32_t(p.G));
     const int64_t rh = orow * p.hq + ohead, sp = int64_t(split) * p.nq * p.hq + rh;
     float sums[DP / TPC] = {};
-    float es = 0.f;
+    float es = 0.f, rs = 0.f;
 #pragma unroll
     for (int pass = 0; pass < (kFix ? 2 : 1); ++pass) {
       __syncthreads();  // the tiles, or the first pass's sums, are read out
@@ -1004,8 +1020,9 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
       __syncthreads();
       if (pass == 0) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) es += le[w * 32 + col];
+        for (int w = 0; w < NW; ++w) es += le[w * 32 + col], rs += le[(NW + w) * 32 + col];
         es *= unit;
+        rs *= unit;
       }
 #pragma unroll
       for (int i = 0; i < DP / TPC; ++i) {
@@ -1019,24 +1036,24 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
           else
             p.part_b[sp * p.d + x] = v * ldexpf(p.scale, -kPExp<T>);
         }
-        sums[i] = pass == 0 ? v : fmaf(-es * punit, v, sums[i]);
+        sums[i] = pass == 0 ? v : fmaf(-rs * punit, v, sums[i]);
       }
     }
     if (!here) return;
     if (e0 == 0 && p.nsplit > 1) {
-      if constexpr (kFix) p.part_e[sp] = es;
+      if constexpr (kFix) p.part_e[2 * sp] = es, p.part_e[2 * sp + 1] = rs;
     }
     if (p.nsplit == 1 && p.dq) {
 #pragma unroll
       for (int i = 0; i < DP / TPC; ++i)
         if (e0 + TPC * i < p.d) static_cast<T*>(p.dq)[rh * p.d + e0 + TPC * i] = T(sums[i] * f);
     }
-    if (e0 == 0 && split == 0) p.delta[int64_t(ohead) * p.nq + orow] = le[NW * 32 + col] + (p.nsplit > 1 ? 0.f : es);
+    if (e0 == 0 && split == 0) p.delta[int64_t(ohead) * p.nq + orow] = le[2 * NW * 32 + col] + (p.nsplit > 1 ? 0.f : es);
     return;
   }
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
-    const float e = kFix ? esum[b] + half_swap(esum[b]) : 0.f;
+    const float e = kFix ? esum[b] + half_swap(esum[b]) : 0.f, re = kFix ? rsum[b] + half_swap(rsum[b]) : 0.f;
     if (!live[b]) continue;
     const int64_t rh = row[b] * p.hq + head[b], at = rh * p.d;
     if (p.nsplit > 1) {
@@ -1046,7 +1063,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
         if constexpr (kFix) store_cols<T, DP>(nullptr, p.part_b + sp * p.d + at, mean[b], p.d, ldexpf(p.scale, -kPExp<T>));
       }
       if (half == 0) {
-        if constexpr (kFix) p.part_e[sp + rh] = e * unit;
+        if constexpr (kFix) p.part_e[2 * (sp + rh)] = e * unit, p.part_e[2 * (sp + rh) + 1] = re * unit;
         if (split == 0) p.delta[int64_t(head[b]) * p.nq + row[b]] = del[b];
       }
       continue;
@@ -1057,25 +1074,29 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
 #pragma unroll
       for (int d = 0; d < TL::kBlocks; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[b][d][r] = fmaf(-(e * unit) * punit, mean[b][d][r], acc[b][d][r]);
+        for (int r = 0; r < 16; ++r) acc[b][d][r] = fmaf(-(re * unit) * punit, mean[b][d][r], acc[b][d][r]);
     store_cols<T, DP>(static_cast<T*>(p.dq) + at, nullptr, acc[b], p.d, f);
   }
 }
 
-// Joins the splits of dQ, in the two forms of the forward join.  e is the sum of the splits' sums of dS (see dq_kernel).
+// Joins the splits of dQ, in the two forms of the forward join.  e and re are the
+// splits' sums of dS and of its rounded values (see dq_kernel).
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
   __shared__ float la[WIDE ? 4 : 1][SSC_MAX_HEAD_DIM], lm[WIDE ? 4 : 1][SSC_MAX_HEAD_DIM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t n = p.nq * p.hq, rh = WIDE ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 4 + wave;
   if (!WIDE && rh >= n) return;
-  float e = 0.f;
+  float e = 0.f, re = 0.f;
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
     for (int i = 0; i < kMaxSplit / 64; ++i)
-      if (lane + 64 * i < p.nsplit) e += p.part_e[(lane + 64 * i) * n + rh];
+      if (lane + 64 * i < p.nsplit) {
+        e += p.part_e[2 * ((lane + 64 * i) * n + rh)];
+        re += p.part_e[2 * ((lane + 64 * i) * n + rh) + 1];
+      }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) e += __shfl_xor(e, d);
+    for (int d = 1; d < 64; d <<= 1) e += __shfl_xor(e, d), re += __shfl_xor(re, d);
     if (lane == 0 && (!WIDE || wave == 0)) p.delta[(rh % p.hq) * p.nq + rh / p.hq] += e;
   }
   if (!p.dq) return;
@@ -1096,12 +1117,12 @@ __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
     const int i = threadIdx.x;
     if (i < p.d) {
       const float as = (la[0][i] + la[1][i]) + (la[2][i] + la[3][i]), mm = (lm[0][i] + lm[1][i]) + (lm[2][i] + lm[3][i]);
-      op[i] = T(fmaf(-e, mm, as));
+      op[i] = T(fmaf(-re, mm, as));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (lane + 64 * i < p.d) op[lane + 64 * i] = T(fmaf(-e, m[i], a[i]));
+      if (lane + 64 * i < p.d) op[lane + 64 * i] = T(fmaf(-re, m[i], a[i]));
   }
 }
 
@@ -1189,7 +1210,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
     if (wave == 0 && lane < R) {
       // rows past the sample and rows with no key: weights 0
       lsh[buf][lane] = lane >= rows || rlse == -INFINITY ? -INFINITY : float(kPExp<T>) - rlse * kLog2e;
-      ldel[buf][lane] = rdel;
+      ldel[buf][lane] = -rdel * dsmul;
     }
   };
   auto scores = [&](int buf, f32x16& s, f32x16& dp) {
@@ -1224,7 +1245,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
       for (int j = 0; j < 4; ++j) {
         const float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * i + j], c, sh[j]));
         s[4 * i + j] = pr;
-        dp[4 * i + j] = pr * scaled<T>(dp[4 * i + j] - de[j], dsmul);
+        dp[4 * i + j] = pr * less_delta<T>(dp[4 * i + j], de[j], dsmul);
       }
     }
 #pragma unroll

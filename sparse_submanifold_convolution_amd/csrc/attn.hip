@@ -78,9 +78,9 @@ BwdPlan bwd_plan(const ssc_attn_shape& a) {
   b.k_tiles = int(a.nk / kc + a.batch + 2);
   b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a);
   // dK and dV of short encoder sequences: few column tiles over long streams, split into several rounds of workgroups
-  // so that the last round's idle CUs and the samples' different lengths matter little.  fp32's blocks are so long
-  // that one workgroup a CU does.
-  const int64_t wgs = busy_wgs(a.nk, kc, a), want = a.dtype == SSC_F32 ? kCUs : 4 * 2 * kCUs;
+  // so that the last round's idle CUs and the samples' different lengths matter little (fp32, whose blocks are long:
+  // half as many rounds).
+  const int64_t wgs = busy_wgs(a.nk, kc, a), want = (a.dtype == SSC_F32 ? 4 : 8) * kCUs;
   b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? 4 : 8);
   return b;
 }
@@ -112,7 +112,7 @@ Ws ws_layout(const ssc_attn_shape& a, bool backward) {
       w.part_q = take(size_t(b.q_split) * qn * d * 4);
       if (a.dtype != SSC_F32) {
         w.mean_q = take(size_t(b.q_split) * qn * d * 4);
-        w.err_q = take(size_t(b.q_split) * qn * 4);
+        w.err_q = take(size_t(b.q_split) * qn * 8);
       }
     }
     if (b.k_split > 1) {
