@@ -5,9 +5,9 @@ wrappers.  Work runs on the current stream of the tensors' device; without the b
 """
 from __future__ import annotations
 
-import ctypes
 import dataclasses
 import math
+import struct
 
 import torch
 
@@ -30,36 +30,28 @@ def _new(like: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
 
 
-class _NormRopeShape(ctypes.Structure):
-    _fields_ = [("n", ctypes.c_int64), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64), ("k_row", ctypes.c_int64),
-                ("k_head", ctypes.c_int64), ("pos_row", ctypes.c_int64), ("heads_q", ctypes.c_int32),
-                ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32), ("norm", ctypes.c_int32),
-                ("weight_per_head", ctypes.c_int32), ("eps", ctypes.c_float)]
-
-
-class _AttnShape(ctypes.Structure):
-    _fields_ = [("nq", ctypes.c_int64), ("nk", ctypes.c_int64), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
-                ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64), ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64),
-                ("batch", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_kv", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+# the C structs of the calls' sizes (include/ssc.h), packed: a bytes object is passed as the pointer to them
+_NORM_ROPE_SHAPE = struct.Struct("=6q9if")
+_ATTN_SHAPE = struct.Struct("=8q5if")
 
 
 def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, n: int | None = None) -> tuple:
-    """(heads, head_dim, row stride, head stride) of a [n, heads, head_dim] view whose heads are 16-byte vectors."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or (n is not None and t.shape[0] != n):
+    """(rows, heads, head_dim, row stride, head stride) of a [n, heads, head_dim] view whose heads are 16-byte vectors."""
+    shape = t.shape
+    if len(shape) != 3 or t.dtype != dtype or t.device != device or (n is not None and shape[0] != n):
         raise ValueError(f"{name}: expected {dtype} [{'n' if n is None else n}, heads, head_dim] on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, heads, dim = t.shape
+                         f"got {t.dtype} {tuple(shape)} on {t.device}")
+    rows, heads, dim = shape
     rs, hs, es = t.stride()
     if rows <= 1:
         rs = 0  # a single row's stride is never used and may be anything
     if heads <= 1:
         hs = 0
-    if dim > 1 and es != 1 or rs * t.element_size() % 16 or hs * t.element_size() % 16 or t.data_ptr() % 16:
+    size = dtype.itemsize
+    if dim > 1 and es != 1 or rs * size % 16 or hs * size % 16 or t.data_ptr() % 16:
         raise ValueError(f"{name}: a head's elements must be contiguous and rows and heads 16-byte aligned, "
                          f"got strides {t.stride()}")
-    return heads, dim, rs, hs
+    return rows, heads, dim, rs, hs
 
 
 def _aligned(t: torch.Tensor) -> bool:
@@ -105,8 +97,8 @@ def _rope_shape(q, k, positions, table, q_weight, k_weight, eps, norm, layout):
         raise SSCError("ssc_qk_norm_rope", 2)
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    hq, dq, qr, qh = _heads(q, "q", dt, dev, n) if q is not None else (0, 0, 0, 0)
-    hk, dk, kr, kh = _heads(k, "k", dt, dev, n) if k is not None else (0, 0, 0, 0)
+    _, hq, dq, qr, qh = _heads(q, "q", dt, dev, n) if q is not None else (0, 0, 0, 0, 0)
+    _, hk, dk, kr, kh = _heads(k, "k", dt, dev, n) if k is not None else (0, 0, 0, 0, 0)
     if q is not None and k is not None and dq != dk:
         raise ValueError(f"queries and keys have head sizes {dq} and {dk}")
     dim = dq or dk
@@ -132,8 +124,8 @@ def _rope_shape(q, k, positions, table, q_weight, k_weight, eps, norm, layout):
         if per_head is not None and per_head != each:
             raise ValueError("q_weight and k_weight: both [heads, head_dim] or both [head_dim]")
         per_head = each
-    sh = _NormRopeShape(n, qr, qh, kr, kh, pos_row, hq, hk, dim, DTYPE_CODE[dt], axes, pairs, ROPE_LAYOUTS[layout],
-                        1 if norm else 0, 1 if per_head else 0, float(eps))
+    sh = _NORM_ROPE_SHAPE.pack(n, qr, qh, kr, kh, pos_row, hq, hk, dim, DTYPE_CODE[dt], axes, pairs,
+                               ROPE_LAYOUTS[layout], 1 if norm else 0, 1 if per_head else 0, eps)
     return sh, dev, dt, (n, hq, dim), (n, hk, dim)
 
 
@@ -153,7 +145,7 @@ def qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None, positions: 
     qo = _new(q) if q is not None else None
     ko = _new(k) if k is not None else None
     _check("ssc_qk_norm_rope_fwd",
-           lib().ssc_qk_norm_rope_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), *_table_ptrs(positions, table),
+           lib().ssc_qk_norm_rope_fwd(sh, _ptr(q), _ptr(k), *_table_ptrs(positions, table),
                                       _ptr(q_weight), _ptr(k_weight), _ptr(qo), _ptr(ko), _stream(dev)))
     return qo, ko
 
@@ -175,12 +167,12 @@ def qk_norm_rope_bwd(q: torch.Tensor | None, k: torch.Tensor | None, positions: 
     dkw = torch.empty_like(k_weight) if need_weights and k_weight is not None and dk_out is not None else None
     ws = None
     if dqw is not None or dkw is not None:
-        nbytes = int(lib().ssc_qk_norm_rope_workspace_bytes(ctypes.byref(sh)))
+        nbytes = int(lib().ssc_qk_norm_rope_workspace_bytes(sh))
         if nbytes == 0:
             raise SSCError("ssc_qk_norm_rope_workspace_bytes", 2)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check("ssc_qk_norm_rope_bwd",
-           lib().ssc_qk_norm_rope_bwd(ctypes.byref(sh), _ptr(q), _ptr(k), *_table_ptrs(positions, table), _ptr(q_weight),
+           lib().ssc_qk_norm_rope_bwd(sh, _ptr(q), _ptr(k), *_table_ptrs(positions, table), _ptr(q_weight),
                                       _ptr(k_weight), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dqw),
                                       _ptr(dkw), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
     return dq, dk, dqw, dkw
@@ -232,10 +224,9 @@ def _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale):
     dev, dt = q.device, q.dtype
     if dt not in DTYPE_CODE:
         raise SSCError("ssc_cross_attn", 2)
-    hq, dim, qr, qh = _heads(q, "q", dt, dev)
-    hk, dim_k, kr, kh = _heads(k, "k", dt, dev)
-    nq, nk = int(q.shape[0]), int(k.shape[0])
-    hv, dim_v, vr, vh = _heads(v, "v", dt, dev, nk)
+    nq, hq, dim, qr, qh = _heads(q, "q", dt, dev)
+    nk, hk, dim_k, kr, kh = _heads(k, "k", dt, dev)
+    _, hv, dim_v, vr, vh = _heads(v, "v", dt, dev, nk)
     if dim_k != dim or dim_v != dim or hv != hk:
         raise ValueError(f"q, k, v: heads and head sizes {tuple(q.shape[1:])}, {tuple(k.shape[1:])}, {tuple(v.shape[1:])} "
                          "do not match")
@@ -248,14 +239,15 @@ def _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale):
         _need(kv_mask, "kv_mask", kv_mask.dtype, (nk,), dev)
     if scale is None:
         scale = dim ** -0.5
-    return _AttnShape(nq, nk, qr, qh, kr, kh, vr, vh, batch, hq, hk, dim, DTYPE_CODE[dt], float(scale)), dev, dt
+    sh = _ATTN_SHAPE.pack(nq, nk, qr, qh, kr, kh, vr, vh, batch, hq, hk, dim, DTYPE_CODE[dt], scale)
+    return sh, dev, dt, (hq, nq)
 
 
 _unused: dict[int, torch.Tensor] = {}  # by device: stands for the workspace of calls that use none
 
 
-def _attn_workspace(sh: _AttnShape, backward: int, dev: torch.device) -> torch.Tensor:
-    nbytes = int(lib().ssc_cross_attn_workspace_bytes(ctypes.byref(sh), backward))
+def _attn_workspace(sh: bytes, backward: int, dev: torch.device) -> torch.Tensor:
+    nbytes = int(lib().ssc_cross_attn_workspace_bytes(sh, backward))
     if nbytes == 0:
         raise SSCError("ssc_cross_attn_workspace_bytes", 2)
     if nbytes == 256 and not backward:  # the smallest size: nothing is kept there
@@ -271,12 +263,12 @@ def cross_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     """ssc_cross_attn_fwd: q [nq, Hq, D] attends k, v [nk, Hk, D] sample by sample -> (out [nq, Hq, D], lse [Hq, nq]).
 
     Offsets are int32 [batch + 1] on the device, kv_mask [nk] bool (True: attended), scale 1 / sqrt(D) by default."""
-    sh, dev, _ = _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
+    sh, dev, _, rows = _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
     ws = _attn_workspace(sh, 0, dev)
     out = _new(q)
-    lse = q.new_empty((sh.heads_q, sh.nq), dtype=torch.float32)
+    lse = q.new_empty(rows, dtype=torch.float32)
     _check("ssc_cross_attn_fwd",
-           lib().ssc_cross_attn_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(q_offsets), _ptr(kv_offsets),
+           lib().ssc_cross_attn_fwd(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(q_offsets), _ptr(kv_offsets),
                                     _ptr(kv_mask), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)))
     return out, lse
 
@@ -286,16 +278,16 @@ def cross_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
                         kv_mask: torch.Tensor | None = None, scale: float | None = None, need_dq: bool = True,
                         need_dk: bool = True, need_dv: bool = True):
     """ssc_cross_attn_bwd: (dq, dk, dv) of cross_attention_fwd; entries not asked for are None."""
-    sh, dev, dt = _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
+    sh, dev, dt, rows = _attn_shape(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
     _need(out, "out", dt, tuple(q.shape), dev)
     _need(dout, "dout", dt, tuple(q.shape), dev)
-    _need(lse, "lse", torch.float32, (sh.heads_q, sh.nq), dev)
+    _need(lse, "lse", torch.float32, rows, dev)
     ws = _attn_workspace(sh, 1, dev)
     dq = torch.empty_like(dout) if need_dq else None
     dk = _new(k) if need_dk else None
     dv = _new(v) if need_dv else None
     _check("ssc_cross_attn_bwd",
-           lib().ssc_cross_attn_bwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+           lib().ssc_cross_attn_bwd(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                                     _ptr(q_offsets), _ptr(kv_offsets), _ptr(kv_mask), _ptr(dq), _ptr(dk), _ptr(dv),
                                     _ptr(ws), ws.numel(), _stream(dev)))
     return dq, dk, dv

@@ -1126,18 +1126,15 @@ __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
   }
 }
 
-// dK and dV of 32 key columns a wave, over 32-row blocks of queries.  The blocks are software pipelined: while block i's
-// probabilities and dS are formed on the vector units, the matrix units work on block i + 1's scores and on block
-// i - 1's products with dout and q, whose operands do not depend on them.  Four LDS tiles in turn let one barrier a
-// block suffice: the tile written for block i + 1 was last read for block i - 3.
+// dK and dV of 32 key columns a wave over tiles of query rows, double buffered in LDS.  Both of a tile's score blocks
+// are formed before the first block's weights, so the matrix units have work while the vector units form those.
 template <typename T, int DP, int NW, bool MASK>
 __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
-  constexpr int R = 32;
-  using TL = TileOf<T, DP, R>;
+  using TL = TileOf<T, DP>;
   using E = Elt<T>;
-  constexpr int NT = NW * 64, TC = NW * 32, KS = E::kSteps;
-  __shared__ __align__(16) char lds[4][2 * TL::kBytes];
-  __shared__ __align__(16) float lsh[4][R], ldel[4][R];
+  constexpr int NT = NW * 64, TC = NW * 32, KS = E::kSteps, R = TL::kRows, G = TL::kGroups;
+  __shared__ __align__(16) char lds[2][2 * TL::kBytes];
+  __shared__ __align__(16) float lsh[2][R], ldel[2][R];
   const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
   if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
   const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
@@ -1162,10 +1159,10 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   // waves whose columns all lie past the sample's keys only help to stage
   const bool busy = sg.tile * TC + wave * 32 < sg.len;
 
-  // the sample's queries, head after head of the group: block n is head n / blocks, rows 32 (n mod blocks) ..
-  const int blocks = (sg.other_len + R - 1) / R;
+  // the sample's queries, head after head of the group: tile n is head n / tiles, its tile n mod tiles
+  const int tiles = (sg.other_len + R - 1) / R;
   int n0, n1;
-  split_range(blocks * p.G, split, p.nsplit, &n0, &n1);
+  split_range(tiles * p.G, split, p.nsplit, &n0, &n1);
   const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
   Walk<R> wq, wd;
   wq.init(p.q_row * int64_t(sizeof(T)), head_bytes);
@@ -1174,7 +1171,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   sq.init(wq.row_bytes, dchunks);
   sd.init(wd.row_bytes, dchunks);
   const float *lse_at = nullptr, *del_at = nullptr;
-  int g = n0 < n1 ? n0 / blocks : 0, left = n0 < n1 ? sg.other_len - (n0 - g * blocks) * R : 0;  // rows of head g to load
+  int g = n0 < n1 ? n0 / tiles : 0, left = n0 < n1 ? sg.other_len - (n0 - g * tiles) * R : 0;  // rows of head g to load
   auto seek = [&]() {
     const int64_t r0 = sg.other + (sg.other_len - left), head = hk * p.G + g;
     wq.at = reinterpret_cast<const char*>(static_cast<const T*>(p.q) + r0 * p.q_row + head * p.q_head);
@@ -1183,7 +1180,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
     del_at = p.delta + head * p.nq + r0;
   };
   float rlse = 0.f, rdel = 0.f;
-  int rows = 0;  // of the block on its way
+  int rows = 0;  // of the tile on its way
   const uint32_t lane_off = wave == 0 && lane < R ? lane * 4 : 0xFFFFFFF0u;
   auto load = [&]() {
     sq.load(wq.at, wq.span(left));
@@ -1213,87 +1210,53 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
       ldel[buf][lane] = -rdel * dsmul;
     }
   };
-  auto scores = [&](int buf, f32x16& s, f32x16& dp) {
-    const char* tq = lds[buf];
-    const char* td = tq + TL::kBytes;
-    s = dp = f32x16{};
-#pragma unroll
-    for (int f = 0; f < TL::kFrags; ++f) {
-      if (TL::skip(f, dchunks)) break;
-      s = E::mma(TL::rows(tq, 0, f), kf[f], s);
-      dp = E::mma(TL::rows(td, 0, f), vf[f], dp);
-    }
-  };
-  auto products = [&](int buf, const u32x4 (&pf)[KS], const u32x4 (&sf)[KS]) {
-    const char* tq = lds[buf];
-    const char* td = tq + TL::kBytes;
-#pragma unroll
-    for (int st = 0; st < KS; ++st)
-#pragma unroll
-      for (int d = 0; d < TL::kBlocks; ++d) {
-        dv[d] = E::mma(TL::cols(td, 0, st, d), pf[st], dv[d]);
-        dk[d] = E::mma(TL::cols(tq, 0, st, d), sf[st], dk[d]);
-      }
-  };
-  auto weights = [&](int buf, f32x16& s, f32x16& dp, u32x4 (&pf)[KS], u32x4 (&sf)[KS]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][8 * i + 4 * half]);
-      const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][8 * i + 4 * half]);
-      const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * i + j], c, sh[j]));
-        s[4 * i + j] = pr;
-        dp[4 * i + j] = pr * less_delta<T>(dp[4 * i + j], de[j], dsmul);
-      }
-    }
-#pragma unroll
-    for (int st = 0; st < KS; ++st) pf[st] = E::pack(s, st), sf[st] = E::pack(dp, st);
-  };
-
-  f32x16 s[2], dp[2];
-  u32x4 pf[2][KS], sf[2][KS];
   const int n = n1 - n0;
   if (n > 0) {
     seek();
     load();
-    // block -1: no weights, and a tile of zeros to multiply them with
-    for (int i = threadIdx.x; i < 2 * TL::kBytes / 16; i += NT) reinterpret_cast<u32x4*>(lds[3])[i] = u32x4{0, 0, 0, 0};
+  }
+  for (int i = 0; i < n; ++i) {
+    const int buf = i & 1;
+    store(buf);
+    __syncthreads();
+    if (i + 1 < n) load();
+    if (!busy) continue;
+    const char* tq = lds[buf];
+    const char* td = tq + TL::kBytes;
+    f32x16 s[G], dp[G];
 #pragma unroll
-    for (int st = 0; st < KS; ++st) pf[1][st] = sf[1][st] = u32x4{0, 0, 0, 0};
-    store(0);
-    if (n > 1) load();
-    __syncthreads();
-  }
-  auto stage = [&](int i) {
-    store((i + 1) & 3);  // past the last block: rows of a block before, whose scores nothing uses
-    __syncthreads();
-    if (i + 2 < n) load();
-  };
-  if (!busy) {
-    for (int i = 0; i < n; ++i) stage(i);
-    return;
-  }
-  if (n > 0) {
-    scores(0, s[0], dp[0]);
-    auto step = [&](int i, f32x16& sc, f32x16& dc, f32x16& sn, f32x16& dn, u32x4 (&pc)[KS], u32x4 (&fc)[KS],
-                    u32x4 (&pp)[KS], u32x4 (&fp)[KS]) {
-      stage(i);
-      scores((i + 1) & 3, sn, dn);
-      products((i + 3) & 3, pp, fp);
-      weights(i & 3, sc, dc, pc, fc);
-    };
-    int i = 0;
-    for (; i + 1 < n; i += 2) {
-      step(i, s[0], dp[0], s[1], dp[1], pf[0], sf[0], pf[1], sf[1]);
-      step(i + 1, s[1], dp[1], s[0], dp[0], pf[1], sf[1], pf[0], sf[0]);
+    for (int b = 0; b < G; ++b) {
+      s[b] = dp[b] = f32x16{};
+#pragma unroll
+      for (int f = 0; f < TL::kFrags; ++f) {
+        if (TL::skip(f, dchunks)) break;
+        s[b] = E::mma(TL::rows(tq, 32 * b, f), kf[f], s[b]);
+        dp[b] = E::mma(TL::rows(td, 32 * b, f), vf[f], dp[b]);
+      }
     }
-    if (i < n) {
-      step(i, s[0], dp[0], s[1], dp[1], pf[0], sf[0], pf[1], sf[1]);
-      products(i & 3, pf[0], sf[0]);
-    } else {
-      products((n - 1) & 3, pf[1], sf[1]);
+#pragma unroll
+    for (int b = 0; b < G; ++b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][32 * b + 8 * i + 4 * half]);
+        const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][32 * b + 8 * i + 4 * half]);
+        const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float pr = __builtin_amdgcn_exp2f(fmaf(s[b][4 * i + j], c, sh[j]));
+          s[b][4 * i + j] = pr;
+          dp[b][4 * i + j] = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
+        }
+      }
+#pragma unroll
+      for (int st = 0; st < KS; ++st) {
+        const u32x4 pf = E::pack(s[b], st), sf = E::pack(dp[b], st);
+#pragma unroll
+        for (int d = 0; d < TL::kBlocks; ++d) {
+          dv[d] = E::mma(TL::cols(td, 32 * b, st, d), pf, dv[d]);
+          dk[d] = E::mma(TL::cols(tq, 32 * b, st, d), sf, dk[d]);
+        }
+      }
     }
   }
 
