@@ -362,7 +362,7 @@ struct Cfg {
   int fwd_qb, fwd_occ, dq_qb, dq_occ, dkv_kb, dkv_occ;
 };
 constexpr Cfg tile_cfg(int esize, int dp) {
-  return dp <= 64 ? Cfg{1, 2, 1, 2, 1, 2} : Cfg{1, esize == 4 ? 1 : 2, 1, 1, 1, 1};
+  return dp <= 64 ? Cfg{1, 2, 1, 2, 1, 2} : Cfg{1, esize == 4 ? 1 : 2, 1, esize == 2 && dp == 96 ? 2 : 1, 1, esize == 2 ? 2 : 1};
 }
 
 // keeps a wave's LDS writes before the reads that follow; the hardware serves them in order
@@ -818,7 +818,8 @@ __device__ __forceinline__ float less_delta(float dp, float ndel, float mul) {
 // none of it.
 template <typename T, int DP, int NW, int QB, bool MASK, bool FEW>
 __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
-  using TL = TileOf<T, DP>;
+  constexpr int R = sizeof(T) == 4 || (!FEW && DP == 96) ? 32 : 64;
+  using TL = TileOf<T, DP, R>;
   using E = Elt<T>;
   constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * QB * 32, BUFS = FEW ? NW : 2;
   constexpr bool kFix = sizeof(T) == 2;
@@ -880,10 +881,10 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
   wv.init(p.v_row * int64_t(sizeof(T)), head_bytes);
   wk.at = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head) + t0 * wk.step;
   wv.at = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head) + t0 * wv.step;
-  Stage<T, DP, NT> sk, sv;
+  Stage<T, DP, NT, R> sk, sv;
   sk.init(wk.row_bytes, dchunks);
   sv.init(wv.row_bytes, dchunks);
-  uint8_t keep[Stage<T, DP, NT>::N];
+  uint8_t keep[Stage<T, DP, NT, R>::N];
   bool kept = false;
   auto load = [&](int t) {
     const int rows = sg.other_len - t * TL::kRows;
@@ -894,8 +895,8 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
     if constexpr (MASK) {
       const uint8_t* mp = p.mask + sg.other + int64_t(t) * TL::kRows;
 #pragma unroll
-      for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
-        const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
+      for (int i = 0; i < Stage<T, DP, NT, R>::N; ++i) {
+        const int r = Stage<T, DP, NT, R>::item(i) / TL::CPR;
         keep[i] = (r < rows && r < TL::kRows) ? mp[r] : 0;
       }
       kept = lane < rows && lane < TL::kRows && mp[lane] != 0;
@@ -1128,11 +1129,12 @@ __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
 
 // dK and dV of 32 key columns a wave over tiles of query rows, double buffered in LDS.  Both of a tile's score blocks
 // are formed before the first block's weights, so the matrix units have work while the vector units form those.
-template <typename T, int DP, int NW, bool MASK>
+template <typename T, int DP, int NW, bool MASK, bool DK, bool DV>
 __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
-  using TL = TileOf<T, DP>;
+  constexpr int R = sizeof(T) == 4 || DP > 64 ? 32 : 64;
+  using TL = TileOf<T, DP, R>;
   using E = Elt<T>;
-  constexpr int NT = NW * 64, TC = NW * 32, KS = E::kSteps, R = TL::kRows, G = TL::kGroups;
+  constexpr int NT = NW * 64, TC = NW * 32, KS = E::kSteps, G = TL::kGroups;
   __shared__ __align__(16) char lds[2][2 * TL::kBytes];
   __shared__ __align__(16) float lsh[2][R], ldel[2][R];
   const int64_t item = xcd_item(int64_t(p.tiles) * p.hk * p.nsplit);
@@ -1150,12 +1152,18 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   const bool live = col < sg.len;
   const int64_t row = sg.begin + (live ? col : 0);
   const bool on = live && (!MASK || p.mask[row] != 0);
-  u32x4 kf[TL::kFrags], vf[TL::kFrags];
+  u32x4 kf[TL::kFrags], vf[DK ? TL::kFrags : 1];
   load_cols<T, DP>(static_cast<const T*>(p.k) + row * p.k_row + hk * p.k_head, on, dchunks, kf);
-  load_cols<T, DP>(static_cast<const T*>(p.v) + row * p.v_row + hk * p.v_head, on, dchunks, vf);
-  f32x16 dk[TL::kBlocks], dv[TL::kBlocks];
+  if constexpr (DK) load_cols<T, DP>(static_cast<const T*>(p.v) + row * p.v_row + hk * p.v_head, on, dchunks, vf);
+  f32x16 dk[DK ? TL::kBlocks : 1], dv[DV ? TL::kBlocks : 1];
+  auto clear = [&]() {
 #pragma unroll
-  for (int d = 0; d < TL::kBlocks; ++d) dk[d] = dv[d] = f32x16{};
+    for (int d = 0; d < TL::kBlocks; ++d) {
+      if constexpr (DK) dk[d] = f32x16{};
+      if constexpr (DV) dv[d] = f32x16{};
+    }
+  };
+  clear();
   // waves whose columns all lie past the sample's keys only help to stage
   const bool busy = sg.tile * TC + wave * 32 < sg.len;
 
@@ -1187,8 +1195,8 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
     sd.load(wd.at, wd.span(left));
     const uint32_t bytes = uint32_t(left < R ? left : R) * 4;
     rlse = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_of(lse_at, bytes), int(lane_off), 0, 0));
-    // dV alone needs no delta, and none was formed
-    if (p.dk) rdel = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_of(del_at, bytes), int(lane_off), 0, 0));
+    // dV alone needs no delta
+    if constexpr (DK) rdel = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_of(del_at, bytes), int(lane_off), 0, 0));
     rows = left;
     left -= R;
     wq.at += wq.step;
@@ -1231,7 +1239,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
       for (int f = 0; f < TL::kFrags; ++f) {
         if (TL::skip(f, dchunks)) break;
         s[b] = E::mma(TL::rows(tq, 32 * b, f), kf[f], s[b]);
-        dp[b] = E::mma(TL::rows(td, 32 * b, f), vf[f], dp[b]);
+        if constexpr (DK) dp[b] = E::mma(TL::rows(td, 32 * b, f), vf[f], dp[b]);
       }
     }
 #pragma unroll
@@ -1239,22 +1247,25 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 sh4 = *reinterpret_cast<const float4*>(&lsh[buf][32 * b + 8 * i + 4 * half]);
-        const float4 de4 = *reinterpret_cast<const float4*>(&ldel[buf][32 * b + 8 * i + 4 * half]);
+        float4 de4{};
+        if constexpr (DK) de4 = *reinterpret_cast<const float4*>(&ldel[buf][32 * b + 8 * i + 4 * half]);
         const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float pr = __builtin_amdgcn_exp2f(fmaf(s[b][4 * i + j], c, sh[j]));
           s[b][4 * i + j] = pr;
-          dp[b][4 * i + j] = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
+          if constexpr (DK) dp[b][4 * i + j] = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
         }
       }
 #pragma unroll
       for (int st = 0; st < KS; ++st) {
-        const u32x4 pf = E::pack(s[b], st), sf = E::pack(dp[b], st);
+        u32x4 pf, sf;
+        if constexpr (DV) pf = E::pack(s[b], st);
+        if constexpr (DK) sf = E::pack(dp[b], st);
 #pragma unroll
         for (int d = 0; d < TL::kBlocks; ++d) {
-          dv[d] = E::mma(TL::cols(td, 32 * b, st, d), pf, dv[d]);
-          dk[d] = E::mma(TL::cols(tq, 32 * b, st, d), sf, dk[d]);
+          if constexpr (DV) dv[d] = E::mma(TL::cols(td, 32 * b, st, d), pf, dv[d]);
+          if constexpr (DK) dk[d] = E::mma(TL::cols(tq, 32 * b, st, d), sf, dk[d]);
         }
       }
     }
@@ -1262,12 +1273,12 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
 
   if (!live) return;
   // a masked key has no gradient, whatever its zeroed column collected
-  if (!on)
-#pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) dk[d] = dv[d] = f32x16{};
+  if (!on) clear();
   const int64_t o = (row * p.hk + hk) * p.d, sp = int64_t(split) * p.nk * p.hk * p.d + o;
-  if (p.dk) store_cols<T, DP>(static_cast<T*>(p.dk) + o, p.nsplit > 1 ? p.part_a + sp : nullptr, dk, p.d, ldexpf(p.scale, -dse));
-  if (p.dv) store_cols<T, DP>(static_cast<T*>(p.dv) + o, p.nsplit > 1 ? p.part_b + sp : nullptr, dv, p.d, ldexpf(1.f, -kPExp<T>));
+  if constexpr (DK)
+    store_cols<T, DP>(static_cast<T*>(p.dk) + o, p.nsplit > 1 ? p.part_a + sp : nullptr, dk, p.d, ldexpf(p.scale, -dse));
+  if constexpr (DV)
+    store_cols<T, DP>(static_cast<T*>(p.dv) + o, p.nsplit > 1 ? p.part_b + sp : nullptr, dv, p.d, ldexpf(1.f, -kPExp<T>));
 }
 
 // dK (blockIdx.y 0) and dV (1): the splits' partial sums added in split order; four elements a thread
@@ -1354,13 +1365,27 @@ void launch_dq_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
     launch_dq_tile<T, DP, 4, tile_cfg(sizeof(T), DP).dq_qb, false>(p, s);
 }
 
-template <typename T, int DP>
-void launch_dkv_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
+template <typename T, int DP, bool DK, bool DV>
+void launch_dkv_tile(const Params& p, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    dkv_kernel<T, DP, 4, true><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, 4, true, DK, DV><<<grid, 256, 0, s>>>(p);
   else
-    dkv_kernel<T, DP, 4, false><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, 4, false, DK, DV><<<grid, 256, 0, s>>>(p);
+}
+
+// The sums of both gradients of a 16-bit head of over 96 leave registers for one wave per SIMD only; a pass for each,
+// which forms the scores again, runs with two (dK and dV of 2 x 11.2k rows, 8 heads of 128: 3.3 -> 2.8 ms).
+template <typename T, int DP>
+void launch_dkv_dim(const Params& p, hipStream_t s) {
+  if constexpr (sizeof(T) == 4 || DP <= 96) {
+    if (p.dk && p.dv) {
+      launch_dkv_tile<T, DP, true, true>(p, s);
+      return;
+    }
+  }
+  if (p.dk) launch_dkv_tile<T, DP, true, false>(p, s);
+  if (p.dv) launch_dkv_tile<T, DP, false, true>(p, s);
 }
 
 template <typename T>
@@ -1424,13 +1449,13 @@ int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s
     p.part_a = w.k_sum;
     p.part_b = w.v_sum;
     if (p.d <= 32)
-      launch_dkv_dim<T, 32>(p, b, s);
+      launch_dkv_dim<T, 32>(p, s);
     else if (p.d <= 64)
-      launch_dkv_dim<T, 64>(p, b, s);
+      launch_dkv_dim<T, 64>(p, s);
     else if (p.d <= 96)
-      launch_dkv_dim<T, 96>(p, b, s);
+      launch_dkv_dim<T, 96>(p, s);
     else
-      launch_dkv_dim<T, 128>(p, b, s);
+      launch_dkv_dim<T, 128>(p, s);
     if (p.nsplit > 1) {
       const int64_t n4 = p.nk * p.hk * p.d / 4;
       sum_splits_kernel<T><<<dim3(unsigned((n4 + 63) / 64), 2), 64, 0, s>>>(w.k_sum, w.v_sum, n4, p.nsplit,

@@ -153,37 +153,55 @@ __global__ void __launch_bounds__(256) rope_fwd(RopeParams p) {
   const int chunk = int(g - row * p.chunks);
   if (row >= p.n) return;
   const bool mine = sub * N < p.d;
-  float co[NA], si[NA];
-#pragma unroll
-  for (int j = 0; j < NA; ++j) co[j] = 1.f, si[j] = 0.f;
-  if (p.pairs > 0) angles<T, HALVES, NA>(p, row, sub, co, si);
   const float inv_d = 1.f / float(p.d);
-  for (int h = chunk; h < p.hq + p.hk; h += p.chunks) {
-    const bool isq = h < p.hq;
-    const int hh = isq ? h : h - p.hq;
-    const T* src = isq ? static_cast<const T*>(p.q) + row * p.q_row + hh * p.q_head
-                       : static_cast<const T*>(p.k) + row * p.k_row + hh * p.k_head;
-    T* dst = isq ? static_cast<T*>(p.qo) + (row * p.hq + hh) * p.d : static_cast<T*>(p.ko) + (row * p.hk + hh) * p.d;
-    const T* w = static_cast<const T*>(isq ? p.qw : p.kw);
-    float f[N];
-    Vec<T>::unpack(mine ? *reinterpret_cast<const u32x4*>(src + sub * N) : u32x4{0, 0, 0, 0}, f);
-    if constexpr (NORM) {
-      float sq = 0.f;
+  const int heads = p.hq + p.hk;
+  float co[NA], si[NA];
+  // heads chunk, chunk + chunks, ...: four at a time, their loads issued together and the first ones' before the angles
+  constexpr int B = 4;
+  for (int h0 = chunk; h0 < heads; h0 += B * p.chunks) {
+    u32x4 v[B];
 #pragma unroll
-      for (int j = 0; j < N; ++j) sq = fmaf(f[j], f[j], sq);
-      const float r = 1.f / sqrtf(group_sum<L>(sq) * inv_d + p.eps);
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] *= r;
-      if (w) {
-        float wf[N];
-        Vec<T>::unpack(mine ? *reinterpret_cast<const u32x4*>(w + (p.per_head ? hh * p.d : 0) + sub * N)
-                            : u32x4{0, 0, 0, 0}, wf);
-#pragma unroll
-        for (int j = 0; j < N; ++j) f[j] *= wf[j];
-      }
+    for (int i = 0; i < B; ++i) {
+      const int h = h0 + i * p.chunks;
+      const bool isq = h < p.hq;
+      const T* src = isq ? static_cast<const T*>(p.q) + row * p.q_row + h * p.q_head
+                         : static_cast<const T*>(p.k) + row * p.k_row + (h - p.hq) * p.k_head;
+      v[i] = u32x4{0, 0, 0, 0};
+      if (mine && h < heads) v[i] = *reinterpret_cast<const u32x4*>(src + sub * N);
     }
-    if (p.pairs > 0) turn<HALVES, false>(f, co, si, p.pairs, sub);
-    if (mine) *reinterpret_cast<u32x4*>(dst + sub * N) = Vec<T>::pack(f);
+    if (h0 == chunk) {
+#pragma unroll
+      for (int j = 0; j < NA; ++j) co[j] = 1.f, si[j] = 0.f;
+      if (p.pairs > 0) angles<T, HALVES, NA>(p, row, sub, co, si);
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int h = h0 + i * p.chunks;
+      if (h >= heads) break;
+      const bool isq = h < p.hq;
+      const int hh = isq ? h : h - p.hq;
+      T* dst = isq ? static_cast<T*>(p.qo) + (row * p.hq + hh) * p.d : static_cast<T*>(p.ko) + (row * p.hk + hh) * p.d;
+      const T* w = static_cast<const T*>(isq ? p.qw : p.kw);
+      float f[N];
+      Vec<T>::unpack(v[i], f);
+      if constexpr (NORM) {
+        float sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) sq = fmaf(f[j], f[j], sq);
+        const float r = 1.f / sqrtf(group_sum<L>(sq) * inv_d + p.eps);
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] *= r;
+        if (w) {
+          float wf[N];
+          Vec<T>::unpack(mine ? *reinterpret_cast<const u32x4*>(w + (p.per_head ? hh * p.d : 0) + sub * N)
+                              : u32x4{0, 0, 0, 0}, wf);
+#pragma unroll
+          for (int j = 0; j < N; ++j) f[j] *= wf[j];
+        }
+      }
+      if (p.pairs > 0) turn<HALVES, false>(f, co, si, p.pairs, sub);
+      if (mine) *reinterpret_cast<u32x4*>(dst + sub * N) = Vec<T>::pack(f);
+    }
   }
 }
 
