@@ -356,15 +356,14 @@ __device__ __forceinline__ void split_range(int tiles, int s, int n, int* first,
   *last = *first + per < tiles ? *first + per : tiles;
 }
 
-// Column blocks of 32 a wave keeps (queries forward and for dQ, keys for dK and dV), and the waves per SIMD the
-// registers are held to.
+// Waves per SIMD the registers are held to.  Two waves overlap their matrix and vector phases: with one (and
+// accumulators in the second register half) the passes ran at 0.5 to 0.7 of their speed.
 struct Cfg {
-  int fwd_qb, fwd_occ, dq_qb, dq_occ, dkv_kb, dkv_occ;
+  int fwd_occ, dq_occ, dkv_occ;
 };
 constexpr Cfg tile_cfg(int esize, int dp) {
-  return dp <= 64 ? Cfg{1, 2, 1, 2, 1, 2} : Cfg{1, esize == 4 ? 1 : 2, 1, esize == 2 && dp == 96 ? 2 : 1, 1, esize == 2 ? 2 : 1};
+  return dp <= 64 ? Cfg{2, 2, 2} : esize == 4 ? Cfg{1, 1, 1} : Cfg{2, dp == 96 ? 2 : 1, 2};
 }
-
 // keeps a wave's LDS writes before the reads that follow; the hardware serves them in order
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -416,14 +415,14 @@ template <typename T>
 constexpr int kFwdExp = __is_same(T, _Float16) ? 8 : 0;
 constexpr float kSlack = 7.f;
 
-// Two forms.  Rows: each wave owns QB * 32 query columns and the workgroup's waves share the streamed tiles, double
+// Two forms.  Rows: each wave owns 32 query columns and the workgroup's waves share the streamed tiles, double
 // buffered in LDS.  FEW (a sample's rows fit 32 columns: single tokens while serving): the waves share the columns and
 // take the tiles in turn, each through an LDS tile of its own with no barrier, and join their sums at the end.
-template <typename T, int DP, int NW, int QB, bool MASK, bool FEW>
-__global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd_occ) fwd_kernel(Params p) {
+template <typename T, int DP, int NW, bool MASK, bool FEW>
+__global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd_occ) fwd_kernel(Params p) {
   using TL = TileOf<T, DP>;
   using E = Elt<T>;
-  constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * QB * 32, BUFS = FEW ? NW : 2;
+  constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * 32, BUFS = FEW ? NW : 2;
   __shared__ __align__(16) char lds[2 * BUFS * TL::kBytes];
   __shared__ unsigned long long lvalid[BUFS];
   __shared__ float lml[FEW ? 2 * NW * 32 : 1];
@@ -441,33 +440,22 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
   const uint32_t flip = p.scale < 0.f ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
 
   // this lane's query columns
-  int64_t row[QB];
-  int head[QB];
-  bool live[QB];
-  u32x4 qf[QB][TL::kFrags];
+  u32x4 qf[TL::kFrags];
+  const uint32_t r = uint32_t(sg.tile) * TC + (FEW ? 0 : wave * 32) + (lane & 31);
+  const bool live = r < uint32_t(sg.len) * uint32_t(p.G);
+  const uint32_t rc = live ? r : 0u, tok = div_g(rc, p);
+  const int64_t row = sg.begin + tok;
+  const int head = hk * p.G + int(rc - tok * uint32_t(p.G));
+  load_cols<T, DP>(static_cast<const T*>(p.q) + row * p.q_row + head * p.q_head, live, dchunks, qf);
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const uint32_t r = uint32_t(sg.tile) * TC + (FEW ? 0 : (wave * QB + b) * 32) + (lane & 31);
-    live[b] = r < uint32_t(sg.len) * uint32_t(p.G);
-    const uint32_t rc = live[b] ? r : 0u, tok = div_g(rc, p);
-    row[b] = sg.begin + tok;
-    head[b] = hk * p.G + int(rc - tok * uint32_t(p.G));
-    load_cols<T, DP>(static_cast<const T*>(p.q) + row[b] * p.q_row + head[b] * p.q_head, live[b], dchunks, qf[b]);
+  for (int f = 0; f < TL::kFrags; ++f)
 #pragma unroll
-    for (int f = 0; f < TL::kFrags; ++f)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) qf[b][f][e] = (qf[b][f][e] & clear) ^ flip;
-  }
+    for (int e = 0; e < 4; ++e) qf[f][e] = (qf[f][e] & clear) ^ flip;
 
-  f32x16 o[QB][TL::kBlocks];
-  float m[QB], l[QB];
+  f32x16 o[TL::kBlocks];
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    m[b] = -INFINITY;
-    l[b] = 0.f;
-#pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) o[b][d] = f32x16{};
-  }
+  for (int d = 0; d < TL::kBlocks; ++d) o[d] = f32x16{};
 
   int t0, t1;
   split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
@@ -527,17 +515,15 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
     if (t + step < t1) load(t + step);
     if (MASK && valid == 0) continue;
 
-    f32x16 s[QB][TL::kGroups];
+    f32x16 s[TL::kGroups];
 #pragma unroll
     for (int kb = 0; kb < TL::kGroups; ++kb) {
-#pragma unroll
-      for (int b = 0; b < QB; ++b) s[b][kb] = f32x16{};
+      s[kb] = f32x16{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
         if (TL::skip(f, dchunks)) break;
         const u32x4 a = TL::rows(lk, 32 * kb, f);
-#pragma unroll
-        for (int b = 0; b < QB; ++b) s[b][kb] = E::mma(a, qf[b][f], s[b][kb]);
+        s[kb] = E::mma(a, qf[f], s[kb]);
       }
     }
     if (valid != kAll) {
@@ -547,54 +533,47 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const bool on = (w >> (8 * (r / 4) + r % 4)) & 1u;
-#pragma unroll
-          for (int b = 0; b < QB; ++b) s[b][kb][r] = on ? s[b][kb][r] : -INFINITY;
+          s[kb][r] = on ? s[kb][r] : -INFINITY;
         }
       }
     }
+    float mx = s[0][0];
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      float mx = s[b][0][0];
+    for (int kb = 0; kb < TL::kGroups; ++kb)
 #pragma unroll
-      for (int kb = 0; kb < TL::kGroups; ++kb)
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb][r]);
+    mx = fmaxf(mx, half_swap(mx)) * c;
+    // The reference point of the exponentials follows the running maximum only when a row's has grown past what the
+    // type holds (2^kSlack): any reference gives the same quotient, and most tiles then skip the rescaling.
+    if (__any(mx > m + kSlack)) {
+      const float mn = fmaxf(m, mx);
+      const float al = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);  // -inf stays: nothing attended yet
+      m = mn;
+      l *= al;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][kb][r]);
-      mx = fmaxf(mx, half_swap(mx)) * c;
-      // The reference point of the exponentials follows the running maximum only when a row's has grown past what the
-      // type holds (2^kSlack): any reference gives the same quotient, and most tiles then skip the rescaling.
-      if (__any(mx > m[b] + kSlack)) {
-        const float mn = fmaxf(m[b], mx);
-        const float al = m[b] == mn ? 1.f : __builtin_amdgcn_exp2f(m[b] - mn);  // -inf stays: nothing attended yet
-        m[b] = mn;
-        l[b] *= al;
+      for (int d = 0; d < TL::kBlocks; ++d)
 #pragma unroll
-        for (int d = 0; d < TL::kBlocks; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[b][d][r] *= al;
-      }
-      const float ref = m[b] == -INFINITY ? 0.f : m[b];
-      const float sh = float(kFwdExp<T>) - ref;
-#pragma unroll
-      for (int kb = 0; kb < TL::kGroups; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[b][kb][r], c, sh));
-          s[b][kb][r] = e;
-          l[b] += e;
-        }
+        for (int r = 0; r < 16; ++r) o[d][r] *= al;
     }
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float sh = float(kFwdExp<T>) - ref;
+#pragma unroll
+    for (int kb = 0; kb < TL::kGroups; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, sh));
+        s[kb][r] = e;
+        l += e;
+      }
 #pragma unroll
     for (int kb = 0; kb < TL::kGroups; ++kb)
 #pragma unroll
       for (int st = 0; st < E::kSteps; ++st) {
-        u32x4 pf[QB];
-#pragma unroll
-        for (int b = 0; b < QB; ++b) pf[b] = E::pack(s[b][kb], st);
+        const u32x4 pf = E::pack(s[kb], st);
 #pragma unroll
         for (int d = 0; d < TL::kBlocks; ++d) {
           const u32x4 a = TL::cols(lv, 32 * kb, st, d);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) o[b][d] = E::mma(a, pf[b], o[b][d]);
+          o[d] = E::mma(a, pf, o[d]);
         }
       }
   }
@@ -602,21 +581,21 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
   if constexpr (FEW) {
     // The waves' references differ: each wave's sums are brought to the largest, then added in wave order.  2 NW
     // threads share a column's elements.
-    float total = l[0] + half_swap(l[0]);
+    float total = l + half_swap(l);
     if (half == 0) {
-      lml[wave * 32 + lane] = m[0];
+      lml[wave * 32 + lane] = m;
       lml[(NW + wave) * 32 + lane] = total;
     }
     __syncthreads();
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) mx = fmaxf(mx, lml[w * 32 + (lane & 31)]);
-    const float al = m[0] == mx ? 1.f : __builtin_amdgcn_exp2f(m[0] - mx);
+    const float al = m == mx ? 1.f : __builtin_amdgcn_exp2f(m - mx);
     float* mine = reinterpret_cast<float*>(lds) + wave * DP * 33;
 #pragma unroll
     for (int d = 0; d < TL::kBlocks; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) mine[(32 * d + 8 * (r / 4) + 4 * half + r % 4) * 33 + (lane & 31)] = o[0][d][r] * al;
+      for (int r = 0; r < 16; ++r) mine[(32 * d + 8 * (r / 4) + 4 * half + r % 4) * 33 + (lane & 31)] = o[d][r] * al;
     __syncthreads();
     constexpr int TPC = 2 * NW;
     const int col = threadIdx.x / TPC, e0 = threadIdx.x % TPC;
@@ -657,24 +636,21 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).fwd
     return;
   }
 
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const float total = l[b] + half_swap(l[b]);
-    if (!live[b]) continue;
-    const bool some = total != 0.f;  // NaN counts
-    if (p.nsplit > 1) {
-      const int64_t at = (int64_t(split) * p.nq + row[b]) * p.hq + head[b];
-      if (half == 0) {
-        p.part_b[2 * at] = m[b];
-        p.part_b[2 * at + 1] = total;
-      }
-      store_cols<T, DP>(nullptr, p.part_a + at * p.d, o[b], p.d, 1.f);
-      continue;
+  const float total = l + half_swap(l);
+  if (!live) return;
+  const bool some = total != 0.f;  // NaN counts
+  if (p.nsplit > 1) {
+    const int64_t at = (int64_t(split) * p.nq + row) * p.hq + head;
+    if (half == 0) {
+      p.part_b[2 * at] = m;
+      p.part_b[2 * at + 1] = total;
     }
-    if (half == 0)
-      p.lse[int64_t(head[b]) * p.nq + row[b]] = some ? (m[b] - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
-    store_cols<T, DP>(static_cast<T*>(p.o) + (row[b] * p.hq + head[b]) * p.d, nullptr, o[b], p.d, some ? 1.f / total : 0.f);
+    store_cols<T, DP>(nullptr, p.part_a + at * p.d, o, p.d, 1.f);
+    return;
   }
+  if (half == 0)
+    p.lse[int64_t(head) * p.nq + row] = some ? (m - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+  store_cols<T, DP>(static_cast<T*>(p.o) + (row * p.hq + head) * p.d, nullptr, o, p.d, some ? 1.f / total : 0.f);
 }
 
 constexpr int kMaxSplit = 128;
@@ -816,12 +792,12 @@ __device__ __forceinline__ float less_delta(float dp, float ndel, float mul) {
 // keys' mean as well (the error of dq against 64 bits fell from twice that of a result only rounded at the end to 1.4
 // times).  The second sum is one more product on operands that are at hand; the dK pass reads delta + e.  fp32 needs
 // none of it.
-template <typename T, int DP, int NW, int QB, bool MASK, bool FEW>
-__global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
+template <typename T, int DP, int NW, bool MASK, bool FEW>
+__global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
   constexpr int R = sizeof(T) == 4 || (!FEW && DP == 96) ? 32 : 64;
   using TL = TileOf<T, DP, R>;
   using E = Elt<T>;
-  constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * QB * 32, BUFS = FEW ? NW : 2;
+  constexpr int NT = FEW ? 64 : NW * 64, TC = FEW ? 32 : NW * 32, BUFS = FEW ? NW : 2;
   constexpr bool kFix = sizeof(T) == 2;
   __shared__ __align__(16) char lds[2 * BUFS * TL::kBytes];
   __shared__ unsigned long long lvalid[BUFS];
@@ -837,38 +813,30 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
   const int dse = ds_exp<T>(p);
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);  // probabilities carry 2^kPExp
 
-  int64_t row[QB];
-  int head[QB];
-  bool live[QB];
-  u32x4 qf[QB][TL::kFrags], df[QB][TL::kFrags];
-  float sh[QB], del[QB], ndel[QB], esum[QB], rsum[QB];
-  f32x16 acc[QB][TL::kBlocks], mean[kFix ? QB : 1][TL::kBlocks];
+  u32x4 qf[TL::kFrags], df[TL::kFrags];
+  f32x16 acc[TL::kBlocks], mean[TL::kBlocks];
+  const uint32_t r = uint32_t(sg.tile) * TC + (FEW ? 0 : wave * 32) + (lane & 31);
+  const bool live = r < uint32_t(sg.len) * uint32_t(p.G);
+  const uint32_t rc = live ? r : 0u, tok = div_g(rc, p);
+  const int64_t row = sg.begin + tok;
+  const int head = hk * p.G + int(rc - tok * uint32_t(p.G));
+  load_cols<T, DP>(static_cast<const T*>(p.q) + row * p.q_row + head * p.q_head, live, dchunks, qf);
+  load_cols<T, DP>(static_cast<const T*>(p.dout) + (row * p.hq + head) * p.d, live, dchunks, df);
+  u32x4 of[TL::kFrags];
+  load_cols<T, DP>(static_cast<const T*>(p.out) + (row * p.hq + head) * p.d, live, dchunks, of);
+  float del = 0.f, esum = 0.f, rsum = 0.f;
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const uint32_t r = uint32_t(sg.tile) * TC + (FEW ? 0 : (wave * QB + b) * 32) + (lane & 31);
-    live[b] = r < uint32_t(sg.len) * uint32_t(p.G);
-    const uint32_t rc = live[b] ? r : 0u, tok = div_g(rc, p);
-    row[b] = sg.begin + tok;
-    head[b] = hk * p.G + int(rc - tok * uint32_t(p.G));
-    load_cols<T, DP>(static_cast<const T*>(p.q) + row[b] * p.q_row + head[b] * p.q_head, live[b], dchunks, qf[b]);
-    load_cols<T, DP>(static_cast<const T*>(p.dout) + (row[b] * p.hq + head[b]) * p.d, live[b], dchunks, df[b]);
-    u32x4 of[TL::kFrags];
-    load_cols<T, DP>(static_cast<const T*>(p.out) + (row[b] * p.hq + head[b]) * p.d, live[b], dchunks, of);
-    float dot = 0.f;
+  for (int f = 0; f < TL::kFrags; ++f)
 #pragma unroll
-    for (int f = 0; f < TL::kFrags; ++f)
+    for (int e = 0; e < 4; ++e) del = E::dot(df[f][e], of[f][e], del);
+  del += half_swap(del);
+  const float ndel = -del * dsmul;
+  const float lse = live ? p.lse[int64_t(head) * p.nq + row] : -INFINITY;
+  const float sh = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;  // rows with no key: probabilities 0
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dot = E::dot(df[b][f][e], of[f][e], dot);
-    del[b] = dot + half_swap(dot);
-    ndel[b] = -del[b] * dsmul;
-    const float lse = live[b] ? p.lse[int64_t(head[b]) * p.nq + row[b]] : -INFINITY;
-    sh[b] = lse == -INFINITY ? -INFINITY : float(kPExp<T>) - lse * kLog2e;  // rows with no key: probabilities 0
-    esum[b] = rsum[b] = 0.f;
-#pragma unroll
-    for (int d = 0; d < TL::kBlocks; ++d) {
-      acc[b][d] = f32x16{};
-      if constexpr (kFix) mean[b][d] = f32x16{};
-    }
+  for (int d = 0; d < TL::kBlocks; ++d) {
+    acc[d] = f32x16{};
+    if constexpr (kFix) mean[d] = f32x16{};
   }
 
   int t0, t1;
@@ -931,59 +899,43 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
     for (int kb = 0; kb < TL::kGroups; ++kb) {
       const uint32_t vw = uint32_t(valid >> (32 * kb));
       if (vw == 0) continue;
-      f32x16 s[QB], dp[QB];
-#pragma unroll
-      for (int b = 0; b < QB; ++b) s[b] = dp[b] = f32x16{};
+      f32x16 s{}, dp{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
         if (TL::skip(f, dchunks)) break;
         const u32x4 a = TL::rows(lk, 32 * kb, f), v = TL::rows(lv, 32 * kb, f);
-#pragma unroll
-        for (int b = 0; b < QB; ++b) {
-          s[b] = E::mma(a, qf[b][f], s[b]);
-          dp[b] = E::mma(v, df[b][f], dp[b]);
-        }
+        s = E::mma(a, qf[f], s);
+        dp = E::mma(v, df[f], dp);
       }
 #pragma unroll
-      for (int b = 0; b < QB; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, sh[b]));
+      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, sh));
       if (~vw != 0) {
         const uint32_t w = vw >> (4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const bool on = (w >> (8 * (r / 4) + r % 4)) & 1u;
-#pragma unroll
-          for (int b = 0; b < QB; ++b) s[b][r] = on ? s[b][r] : 0.f;
+          s[r] = on ? s[r] : 0.f;
         }
       }
 #pragma unroll
-      for (int b = 0; b < QB; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          dp[b][r] = s[b][r] * less_delta<T>(dp[b][r], ndel[b], dsmul);
-          if constexpr (kFix) esum[b] += dp[b][r];
-        }
+      for (int r = 0; r < 16; ++r) {
+        dp[r] = s[r] * less_delta<T>(dp[r], ndel, dsmul);
+        if constexpr (kFix) esum += dp[r];
+      }
 #pragma unroll
       for (int st = 0; st < E::kSteps; ++st) {
-        u32x4 pf[QB], sf[QB];
+        const u32x4 sf = E::pack(dp, st);
+        u32x4 pf;
+        if constexpr (kFix) {
+          pf = E::pack(s, st);
 #pragma unroll
-        for (int b = 0; b < QB; ++b) {
-          sf[b] = E::pack(dp[b], st);
-          if constexpr (kFix) {
-            pf[b] = E::pack(s[b], st);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) rsum[b] = E::sum(sf[b][j], rsum[b]);
-          }
+          for (int j = 0; j < 4; ++j) rsum = E::sum(sf[j], rsum);
         }
 #pragma unroll
         for (int d = 0; d < TL::kBlocks; ++d) {
           const u32x4 a = TL::cols(lk, 32 * kb, st, d);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) {
-            acc[b][d] = E::mma(a, sf[b], acc[b][d]);
-            if constexpr (kFix) mean[b][d] = E::mma(a, pf[b], mean[b][d]);
-          }
+          acc[d] = E::mma(a, sf, acc[d]);
+          if constexpr (kFix) mean[d] = E::mma(a, pf, mean[d]);
         }
       }
     }
@@ -994,11 +946,11 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
     // the waves' sums, added in wave order; 2 NW threads share a column's elements
     float* all = reinterpret_cast<float*>(lds);
     float* mine = all + wave * DP * 33;
-    const float e = kFix ? esum[0] + half_swap(esum[0]) : 0.f, re = kFix ? rsum[0] + half_swap(rsum[0]) : 0.f;
+    const float e = kFix ? esum + half_swap(esum) : 0.f, re = kFix ? rsum + half_swap(rsum) : 0.f;
     if (half == 0) {
       le[wave * 32 + lane] = e;
       le[(NW + wave) * 32 + lane] = re;
-      if (wave == 0) le[2 * NW * 32 + lane] = del[0];
+      if (wave == 0) le[2 * NW * 32 + lane] = del;
     }
     constexpr int TPC = 2 * NW;
     const int col = threadIdx.x / TPC, e0 = threadIdx.x % TPC;
@@ -1017,7 +969,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
       for (int d = 0; d < TL::kBlocks; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          mine[(32 * d + 8 * (i / 4) + 4 * half + i % 4) * 33 + (lane & 31)] = pass == 0 ? acc[0][d][i] : mean[0][d][i];
+          mine[(32 * d + 8 * (i / 4) + 4 * half + i % 4) * 33 + (lane & 31)] = pass == 0 ? acc[d][i] : mean[d][i];
       __syncthreads();
       if (pass == 0) {
 #pragma unroll
@@ -1052,32 +1004,29 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 1 : tile_cfg(sizeof(T), DP).dq_
     if (e0 == 0 && split == 0) p.delta[int64_t(ohead) * p.nq + orow] = le[2 * NW * 32 + col] + (p.nsplit > 1 ? 0.f : es);
     return;
   }
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const float e = kFix ? esum[b] + half_swap(esum[b]) : 0.f, re = kFix ? rsum[b] + half_swap(rsum[b]) : 0.f;
-    if (!live[b]) continue;
-    const int64_t rh = row[b] * p.hq + head[b], at = rh * p.d;
-    if (p.nsplit > 1) {
-      const int64_t sp = int64_t(split) * p.nq * p.hq;
-      if (p.dq) {
-        store_cols<T, DP>(nullptr, p.part_a + sp * p.d + at, acc[b], p.d, f);
-        if constexpr (kFix) store_cols<T, DP>(nullptr, p.part_b + sp * p.d + at, mean[b], p.d, ldexpf(p.scale, -kPExp<T>));
-      }
-      if (half == 0) {
-        if constexpr (kFix) p.part_e[2 * (sp + rh)] = e * unit, p.part_e[2 * (sp + rh) + 1] = re * unit;
-        if (split == 0) p.delta[int64_t(head[b]) * p.nq + row[b]] = del[b];
-      }
-      continue;
+  const float e = kFix ? esum + half_swap(esum) : 0.f, re = kFix ? rsum + half_swap(rsum) : 0.f;
+  if (!live) return;
+  const int64_t rh = row * p.hq + head, at = rh * p.d;
+  if (p.nsplit > 1) {
+    const int64_t sp = int64_t(split) * p.nq * p.hq;
+    if (p.dq) {
+      store_cols<T, DP>(nullptr, p.part_a + sp * p.d + at, acc, p.d, f);
+      if constexpr (kFix) store_cols<T, DP>(nullptr, p.part_b + sp * p.d + at, mean, p.d, ldexpf(p.scale, -kPExp<T>));
     }
-    if (half == 0) p.delta[int64_t(head[b]) * p.nq + row[b]] = del[b] + e * unit;
-    if (!p.dq) continue;
-    if constexpr (kFix)
-#pragma unroll
-      for (int d = 0; d < TL::kBlocks; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[b][d][r] = fmaf(-(re * unit) * punit, mean[b][d][r], acc[b][d][r]);
-    store_cols<T, DP>(static_cast<T*>(p.dq) + at, nullptr, acc[b], p.d, f);
+    if (half == 0) {
+      if constexpr (kFix) p.part_e[2 * (sp + rh)] = e * unit, p.part_e[2 * (sp + rh) + 1] = re * unit;
+      if (split == 0) p.delta[int64_t(head) * p.nq + row] = del;
+    }
+    return;
   }
+  if (half == 0) p.delta[int64_t(head) * p.nq + row] = del + e * unit;
+  if (!p.dq) return;
+  if constexpr (kFix)
+#pragma unroll
+    for (int d = 0; d < TL::kBlocks; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[d][r] = fmaf(-(re * unit) * punit, mean[d][r], acc[d][r]);
+  store_cols<T, DP>(static_cast<T*>(p.dq) + at, nullptr, acc, p.d, f);
 }
 
 // Joins the splits of dQ, in the two forms of the forward join.  e and re are the
@@ -1331,38 +1280,38 @@ int launch_bwd(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s);
 // launches
 // ---------------------------------------------------------------------------
 
-template <typename T, int DP, int NW, int QB, bool FEW>
+template <typename T, int DP, bool FEW>
 void launch_fwd_tile(const Params& p, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    fwd_kernel<T, DP, NW, QB, true, FEW><<<grid, NW * 64, 0, s>>>(p);
+    fwd_kernel<T, DP, 4, true, FEW><<<grid, 256, 0, s>>>(p);
   else
-    fwd_kernel<T, DP, NW, QB, false, FEW><<<grid, NW * 64, 0, s>>>(p);
+    fwd_kernel<T, DP, 4, false, FEW><<<grid, 256, 0, s>>>(p);
 }
 
 template <typename T, int DP>
 void launch_fwd_dim(const Params& p, const FwdPlan& f, hipStream_t s) {
   if (f.few)
-    launch_fwd_tile<T, DP, 4, 1, true>(p, s);
+    launch_fwd_tile<T, DP, true>(p, s);
   else
-    launch_fwd_tile<T, DP, 4, tile_cfg(sizeof(T), DP).fwd_qb, false>(p, s);
+    launch_fwd_tile<T, DP, false>(p, s);
 }
 
-template <typename T, int DP, int NW, int QB, bool FEW>
+template <typename T, int DP, bool FEW>
 void launch_dq_tile(const Params& p, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    dq_kernel<T, DP, NW, QB, true, FEW><<<grid, NW * 64, 0, s>>>(p);
+    dq_kernel<T, DP, 4, true, FEW><<<grid, 256, 0, s>>>(p);
   else
-    dq_kernel<T, DP, NW, QB, false, FEW><<<grid, NW * 64, 0, s>>>(p);
+    dq_kernel<T, DP, 4, false, FEW><<<grid, 256, 0, s>>>(p);
 }
 
 template <typename T, int DP>
 void launch_dq_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
   if (b.q_few)
-    launch_dq_tile<T, DP, 4, 1, true>(p, s);
+    launch_dq_tile<T, DP, true>(p, s);
   else
-    launch_dq_tile<T, DP, 4, tile_cfg(sizeof(T), DP).dq_qb, false>(p, s);
+    launch_dq_tile<T, DP, false>(p, s);
 }
 
 template <typename T, int DP, bool DK, bool DV>

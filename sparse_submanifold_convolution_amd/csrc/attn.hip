@@ -37,10 +37,6 @@ int pick_split(int64_t wgs, int64_t want, int64_t stream_tiles, int64_t least) {
   return n < 1 ? 1 : int(n);
 }
 
-Cfg cfg_of(const ssc_attn_shape& a) {
-  return tile_cfg(esize(a.dtype), a.head_dim <= 32 ? 32 : a.head_dim <= 64 ? 64 : a.head_dim <= 96 ? 96 : 128);
-}
-
 // workgroups of a pass: its tiles (an average over the samples) and heads
 int64_t busy_wgs(int64_t rows, int64_t cols, const ssc_attn_shape& a) {
   const int64_t tiles = ceil_div(rows, cols);
@@ -61,7 +57,7 @@ FwdPlan fwd_plan(const ssc_attn_shape& a) {
   const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype)));
   FwdPlan f{};
   f.few = rows <= 32 * int64_t(a.batch);
-  const int64_t cols = f.few ? 32 : 4 * 32 * cfg_of(a).fwd_qb;
+  const int64_t cols = f.few ? 32 : 128;
   f.tiles = int(rows / cols + a.batch + 2);
   f.nsplit = row_split(f.few, busy_wgs(rows, cols, a), kv_tiles, a);
   return f;
@@ -73,7 +69,7 @@ BwdPlan bwd_plan(const ssc_attn_shape& a) {
   const int64_t q_tiles = ceil_div(ceil_div(rows, a.batch), tile_rows(esize(a.dtype)));
   BwdPlan b{};
   b.q_few = rows <= 32 * int64_t(a.batch);
-  const int64_t qc = b.q_few ? 32 : 4 * 32 * cfg_of(a).dq_qb, kc = 4 * 32 * cfg_of(a).dkv_kb;
+  const int64_t qc = b.q_few ? 32 : 128, kc = 128;
   b.q_tiles = int(rows / qc + a.batch + 2);
   b.k_tiles = int(a.nk / kc + a.batch + 2);
   b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a);
