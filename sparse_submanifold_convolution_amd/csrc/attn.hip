@@ -77,7 +77,7 @@ BwdPlan bwd_plan(const ssc_attn_shape& a) {
   // so that the last round's idle CUs and the samples' different lengths matter little (fp32, whose blocks are long:
   // half as many rounds).
   const int64_t wgs = busy_wgs(a.nk, kc, a), want = (a.dtype == SSC_F32 ? 4 : 8) * kCUs;
-  b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? 4 : 8);
+  b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? 2 : 8);
   return b;
 }
 

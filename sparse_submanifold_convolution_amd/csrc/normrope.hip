@@ -398,9 +398,9 @@ template <typename T, int L, bool HALVES>
 void fwd_lanes(const ssc_norm_rope_shape& a, RopeParams& p, hipStream_t s) {
   const int heads = a.heads_q + a.heads_kv;
   // Heads a group walks: up to 8 (the angles are then a small part of its work), fewer when the rows alone do not
-  // give the chip's 65536 groups of 8 lanes
+  // give the chip 4096 waves (22.4k rows x 8 heads: 14.7 us with twice as many, 13.4 us)
   int64_t chunks = (heads + 7) / 8;
-  while (chunks < heads && a.n * chunks * L < 524288) chunks *= 2;
+  while (chunks < heads && a.n * chunks * L < 262144) chunks *= 2;
   if (chunks > heads) chunks = heads;
   p.chunks = int32_t(chunks);
   const int64_t threads = a.n * chunks * L;
