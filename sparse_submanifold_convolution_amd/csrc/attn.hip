@@ -57,7 +57,7 @@ FwdPlan fwd_plan(const ssc_attn_shape& a) {
   const int64_t kv_tiles = ceil_div(ceil_div(a.nk, a.batch), tile_rows(esize(a.dtype)));
   FwdPlan f{};
   f.few = rows <= 32 * int64_t(a.batch);
-  const int64_t cols = f.few ? 32 : 128;
+  const int64_t cols = f.few ? 32 : 32 * fwd_waves(esize(a.dtype), a.head_dim > 96 ? 128 : 96);
   f.tiles = int(rows / cols + a.batch + 2);
   f.nsplit = row_split(f.few, busy_wgs(rows, cols, a), kv_tiles, a);
   return f;
