@@ -419,9 +419,16 @@ template <typename T>
 constexpr int kFwdExp = __is_same(T, _Float16) ? 8 : 0;
 constexpr float kSlack = 7.f;
 
-// Two forms.  Rows: each wave owns 32 query columns and the workgroup's waves share the streamed tiles, double
-// buffered in LDS.  FEW (a sample's rows fit 32 columns: single tokens while serving): the waves share the columns and
-// take the tiles in turn, each through an LDS tile of its own with no barrier, and join their sums at the end.
+// Online softmax: per tile of keys s = q k^T, the reference m follows the row's maximum, p = 2^(c s - m), l += sum p,
+// o += p v; out = o / l and lse = m + ln l.  A wave keeps 32 query columns: their fragments, sums and statistics are
+// registers, and one tile of 64 keys costs it 16 MFMA (head of 64) against about 200 vector instructions, so both units
+// bound it, and power: self attention of 2 x 11.2k rows, 16 heads of 64, bf16, takes 1.15 ms (0.9 PFLOP/s; MFMA 44 %
+// and vector issue 70 % of the cycles), 22.4k rows over 4,099 keys, 8 heads of 128, fp16, 0.40 ms (0.93 PFLOP/s).
+//
+// Two forms.  Rows: the workgroup's waves own different columns and share the streamed tiles, double buffered in LDS
+// with one barrier a tile.  FEW (a sample's rows fit 32 columns: single tokens while serving): the waves share the
+// columns and take the tiles in turn, each through an LDS tile of its own with no barrier, and join their sums at the
+// end; four rows pooling 0.8M keys, 4 heads of 64, run at 5.2 TB/s.
 template <typename T, int DP, int NW, bool MASK, bool FEW>
 __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd_occ) fwd_kernel(Params p) {
   using TL = TileOf<T, DP>;
@@ -789,13 +796,17 @@ __device__ __forceinline__ float less_delta(float dp, float ndel, float mul) {
   return kPExp<T> == 0 ? dp + ndel : fmaf(dp, mul, ndel);
 }
 
-// dQ, and the exact delta.  The forward result that delta = dout . out is formed from was rounded to 16 bits, and that
-// error meets every key of the row with one sign: where attention is peaked it outweighs dS itself.  The sum of a row's
-// dS is zero, so the sum e of the dS formed with the rounded delta is the error, and dq = scale (sum dS k - e sum P k).
-// With the sum of the values of dS as they are rounded for the product in e's place, their rounding goes out along the
-// keys' mean as well (the error of dq against 64 bits fell from twice that of a result only rounded at the end to 1.4
-// times).  The second sum is one more product on operands that are at hand; the dK pass reads delta + e.  fp32 needs
-// none of it.
+// dq_i = scale sum_j dS_ij k_j, and the exact delta.  The forward result that delta = dout . out is formed from was
+// rounded to 16 bits, and that error meets every key of the row with one sign: where attention is peaked it outweighs dS
+// itself.  The sum of a row's dS is zero, so the sum e of the dS formed with the rounded delta is the error, and
+// dq = scale (sum dS k - e sum P k).  With the sum of the values of dS as they are rounded for the product in e's place,
+// their rounding goes out along the keys' mean as well (the error of dq against 64 bits fell from 2.1 to 1.4 times that
+// of a result only rounded at the end, for about 5 % of this pass).  The second sum is one more product on operands that
+// are at hand; the dK pass reads delta + e.  fp32 needs none of it.
+//
+// Forms, tiles and bounds as the forward pass: 2 x 11.2k rows, 16 heads of 64, bf16, 2.0 ms (four products at
+// 1.0 PFLOP/s, MFMA busy 48 % of the cycles).  Heads of 72 to 96 stream 32-row tiles, whose smaller stage leaves
+// registers for a second wave per SIMD (8 heads of 96: 1.8 -> 1.5 ms).
 template <typename T, int DP, int NW, bool MASK, bool FEW>
 __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
   constexpr int R = sizeof(T) == 4 || (!FEW && DP == 96) ? 32 : 64;
@@ -1080,8 +1091,12 @@ __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
   }
 }
 
-// dK and dV of 32 key columns a wave over tiles of query rows, double buffered in LDS.  Both of a tile's score blocks
-// are formed before the first block's weights, so the matrix units have work while the vector units form those.
+// dv_j = sum_i P_ij dout_i and dk_j = scale sum_i dS_ij q_i of 32 key columns a wave, over tiles of query rows (head after
+// head of the group), double buffered in LDS.  Both of a tile's score blocks are formed before the first block's
+// weights, so the matrix units have work while the vector units form those.  Bound as the forward pass, with 32 MFMA a
+// tile: 2 x 11.2k rows, 16 heads of 64, bf16, 2.0 ms (four products at 1.0 PFLOP/s, MFMA busy 49 % of the cycles).  A
+// software pipeline over 32-row blocks measured the same for heads of 64 and 10 to 60 % longer for 32 and for fp32.
+// DK, DV: the gradients a launch forms.
 template <typename T, int DP, int NW, bool MASK, bool DK, bool DV>
 __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
   constexpr int R = sizeof(T) == 4 || DP > 64 ? 32 : 64;

@@ -11,7 +11,8 @@
 // row's cosines and sines are computed once per group.  Turns are multiplied and reduced to [-1/2, 1/2] in 64 bits:
 // the phase of a position near 2^31 is as exact as that of position 1.  Sums, the norm and the rotation are fp32 and
 // the result is rounded once.  The calls are bound by memory: each element is read once and written once (backward:
-// read twice, written once).
+// read twice, written once).  629k rows of 16 + 16 heads of 64, bf16: forward 0.95 ms (5.4 TB/s), backward 1.50 ms
+// (5.2 TB/s); a 1 GiB copy reaches 5.2 TB/s.
 
 #include <hip/hip_runtime.h>
 
@@ -143,7 +144,7 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Lanes of one group that hold a vector; the others compute on zeros and store nothing.
+// Lanes of a group past the head's vectors compute on zeros and store nothing.
 template <typename T, int L, bool HALVES, bool NORM>
 __global__ void __launch_bounds__(256) rope_fwd(RopeParams p) {
   constexpr int N = Vec<T>::N, NA = HALVES ? N : N / 2;
@@ -207,7 +208,9 @@ __global__ void __launch_bounds__(256) rope_fwd(RopeParams p) {
 
 constexpr int kRopeHeads = 4;  // heads a backward group keeps weight-gradient sums for
 
-// blockIdx.y: heads y * kRopeHeads ..; the block's groups take rows in turn and the sums stay in registers
+// blockIdx.y: heads y * kRopeHeads ..; the block's groups take rows in turn and the weight gradients' sums stay in
+// registers.  All loads of a row's heads are issued before its angles are formed: with a head's loads waited for one
+// after another the pass ran at 3.0 TB/s.
 template <typename T, int L, bool HALVES, bool NORM, bool DW>
 __global__ void __launch_bounds__(256) rope_bwd(RopeParams p) {
   constexpr int N = Vec<T>::N, NA = HALVES ? N : N / 2, GPB = 256 / L;
