@@ -21,7 +21,9 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(device: torch.device) -> int:
-    # the handle itself: a Stream object costs more than a small call's kernel
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
+    # the handle itself: making a Stream object takes about 2 us
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 

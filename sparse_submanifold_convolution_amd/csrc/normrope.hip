@@ -373,6 +373,8 @@ int rope_check(const ssc_norm_rope_shape* a) {
   if (a->layout != SSC_ROPE_INTERLEAVED && a->layout != SSC_ROPE_HALVES) return SSC_ERR_UNSUPPORTED;
   if (a->layout == SSC_ROPE_HALVES && a->pairs % vec != 0) return SSC_ERR_UNSUPPORTED;
   if (a->norm && !(a->eps >= 0.f && a->eps < INFINITY)) return SSC_ERR_INVALID_ARG;
+  // groups of up to 64 lanes, at least one for every eight heads of a row, in workgroups of 256
+  if (a->n * ((a->heads_q + a->heads_kv + 7) / 8) / 4 >= (1LL << 31) - 1) return SSC_ERR_UNSUPPORTED;
   const int64_t st[4] = {a->q_row_stride, a->q_head_stride, a->k_row_stride, a->k_head_stride};
   for (int64_t v : st)
     if (v < 0 || v > (1LL << 40) || v % vec != 0) return SSC_ERR_INVALID_ARG;

@@ -143,3 +143,20 @@ def test_attention_python_checks():
         ssc.qk_norm_rope_fwd(None, None)
     with pytest.raises(ValueError):
         ssc.rope_table((4, -1), device="cpu")
+
+
+def test_norm_rope_refuses_a_launch_past_the_grid(L):
+    # 2^28 rows of 2,048 heads: more workgroups than a launch takes
+    assert L.ssc_qk_norm_rope_workspace_bytes(_rope(n=1 << 28, hq=1024, hk=1024)) == 0
+
+
+def test_attention_refuses_tensors_off_the_gpu():
+    import torch
+
+    import sparse_submanifold_convolution_amd as ssc
+    q = torch.zeros(4, 2, 64)
+    off = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ssc.cross_attention_fwd(q, q, q, off, off)
+    with pytest.raises(ValueError):
+        ssc.qk_norm_rope_fwd(q, q)

@@ -341,3 +341,46 @@ def test_key_rows_past_32_bit_offsets(ssc):
         return gq, kk, vv
 
     _check(ssc, (q, k, v, do, qo, ko, None), views=views)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_broadcast_rows(ssc, dt):
+    """Rows of stride 0: one query row for all, one key row for all, past a tile's end as well."""
+    q, k, v, do, qo, ko, _ = _to(*_inputs(18, [50, 20], [70, 33], 2, 2, 64, dt))
+    for name in ("q", "k", "v"):
+        t = {"q": q, "k": k, "v": v}
+        t[name] = t[name][:1].expand(t[name].shape)
+        assert t[name].stride(0) == 0
+        results = []
+        for u in (t, {n: x.contiguous() for n, x in t.items()}):
+            out, lse = ssc.cross_attention_fwd(u["q"], u["k"], u["v"], qo, ko)
+            results.append((out, lse, *ssc.cross_attention_bwd(u["q"], u["k"], u["v"], out, lse, do, qo, ko)))
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
+
+
+def test_offsets_outside_the_rows_are_clamped(ssc):
+    q, k, v, do, _, _, _ = _to(*_inputs(19, [40], [60], 2, 2, 32, "bf16"))
+
+    def run(qo, ko):
+        qo, ko = (torch.tensor(o, dtype=torch.int32, device=DEV) for o in (qo, ko))
+        out, lse = ssc.cross_attention_fwd(q, k, v, qo, ko)
+        return (out, lse, *ssc.cross_attention_bwd(q, k, v, out, lse, do, qo, ko))
+
+    for a, b in zip(run([-5, 30, 1 << 30], [-(1 << 31), 25, 100]), run([0, 30, 40], [0, 25, 60])):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_sum_of_value_gradients(ssc, dt, d):
+    """A row's probabilities sum to one: the value gradients of a sample sum to the sum of its output gradients."""
+    q, k, v, do, qo, ko, _ = _to(*_inputs(20, [300], [200], 1, 1, d, dt))
+    out, lse = ssc.cross_attention_fwd(q, k, v, qo, ko)
+    _, _, dv = ssc.cross_attention_bwd(q, k, v, out, lse, do, qo, ko)
+    got, ref = dv.double().sum(0), do.double().sum(0)
+    # each of the n entries is off by u of itself, and by u and some fp32 steps of sum P |dout|; the sums of those are
+    # at most the sum of |dout| each
+    u = _u(dt)
+    tol = (2 * u + 2 ** -14) * do.double().abs().sum(0) + (200 * 2.0 ** -25 if dt == "f16" else 0)
+    assert ((got - ref).abs() <= tol).all()
