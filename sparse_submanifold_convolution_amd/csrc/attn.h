@@ -419,6 +419,14 @@ template <typename T>
 constexpr int kFwdExp = __is_same(T, _Float16) ? 8 : 0;
 constexpr float kSlack = 7.f;
 
+// factor from scores, and their maxima, to exponents of two
+__device__ __forceinline__ float exp_unit(const Params& p) { return p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e; }
+// ln sum exp of a row from its reference score and its sum
+template <typename T>
+__device__ __forceinline__ float lse_of(const Params& p, float m, float total) {
+  return fmaf(m, fabsf(p.scale), logf(total) - float(kFwdExp<T>) * kLn2);
+}
+
 // Online softmax: per tile of keys s = q k^T, the reference m follows the row's maximum, p = 2^(c s - m), l += sum p,
 // o += p v; out = o / l and lse = m + ln l.  A wave keeps 32 query columns: their fragments, sums and statistics are
 // registers, and one tile of 64 keys costs it 16 MFMA (head of 64) against about 200 vector instructions, so both units
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
   const int dchunks = p.d / TL::kVec;
   // the running maximum is taken on unscaled scores: a negative scale's sign goes into the queries (exactly), and a
   // scale of zero clears them (a masked score's -inf times 0 would be NaN)
-  const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
+  const float c = exp_unit(p);
   const uint32_t clear = p.scale == 0.f ? 0u : ~0u;
   const uint32_t flip = p.scale < 0.f ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
 
@@ -553,12 +561,12 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
     for (int kb = 0; kb < TL::kGroups; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb][r]);
-    mx = fmaxf(mx, half_swap(mx)) * c;
+    mx = fmaxf(mx, half_swap(mx));
     // The reference point of the exponentials follows the running maximum only when a row's has grown past what the
     // type holds (2^kSlack): any reference gives the same quotient, and most tiles then skip the rescaling.
-    if (__any(mx > m + kSlack)) {
+    if (__any((mx - m) * c > kSlack)) {
       const float mn = fmaxf(m, mx);
-      const float al = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);  // -inf stays: nothing attended yet
+      const float al = m == mn ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);  // -inf stays: nothing attended yet
       m = mn;
       l *= al;
 #pragma unroll
@@ -567,12 +575,13 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
         for (int r = 0; r < 16; ++r) o[d][r] *= al;
     }
     const float ref = m == -INFINITY ? 0.f : m;
-    const float sh = float(kFwdExp<T>) - ref;
+    const float sh = float(kFwdExp<T>) - ref * c;
 #pragma unroll
     for (int kb = 0; kb < TL::kGroups; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(s[kb][r], c, sh));
+        // fp32 subtracts before it scales, which rounds the difference and not the score
+        const float e = __builtin_amdgcn_exp2f(sizeof(T) == 4 ? (s[kb][r] - ref) * c : fmaf(s[kb][r], c, sh));
         s[kb][r] = e;
         l += e;
       }
@@ -601,7 +610,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) mx = fmaxf(mx, lml[w * 32 + (lane & 31)]);
-    const float al = m == mx ? 1.f : __builtin_amdgcn_exp2f(m - mx);
+    const float al = m == mx ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
     float* mine = reinterpret_cast<float*>(lds) + wave * DP * 33;
 #pragma unroll
     for (int d = 0; d < TL::kBlocks; ++d)
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float mw = lml[w * 32 + col];
-      total += lml[(NW + w) * 32 + col] * (mw == mx ? 1.f : __builtin_amdgcn_exp2f(mw - mx));
+      total += lml[(NW + w) * 32 + col] * (mw == mx ? 1.f : __builtin_amdgcn_exp2f((mw - mx) * c));
     }
     const bool some = total != 0.f;  // NaN counts
     const float inv = p.nsplit > 1 ? 1.f : (some ? 1.f / total : 0.f);
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
         p.part_b[2 * at] = mx;
         p.part_b[2 * at + 1] = total;
       } else {
-        p.lse[int64_t(ohead) * p.nq + orow] = some ? (mx - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+        p.lse[int64_t(ohead) * p.nq + orow] = some ? lse_of<T>(p, mx, total) : -INFINITY;
       }
     }
     return;
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
     return;
   }
   if (half == 0)
-    p.lse[int64_t(head) * p.nq + row] = some ? (m - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+    p.lse[int64_t(head) * p.nq + row] = some ? lse_of<T>(p, m, total) : -INFINITY;
   store_cols<T, DP>(static_cast<T*>(p.o) + (row * p.hq + head) * p.d, nullptr, o, p.d, some ? 1.f / total : 0.f);
 }
 
@@ -691,7 +700,7 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
   float total = 0.f;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
-    const float w = ms[i] == mx ? 1.f : __builtin_amdgcn_exp2f(ms[i] - mx);
+    const float w = ms[i] == mx ? 1.f : __builtin_amdgcn_exp2f((ms[i] - mx) * exp_unit(p));
     total += w * ls[i];
     lw[wave][lane + 64 * i] = w;
   }
@@ -721,7 +730,7 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
       if (lane + 64 * e < p.d) op[lane + 64 * e] = T(acc[e] * inv);
   }
   if (lane == 0 && (!WIDE || wave == 0))
-    p.lse[(rh % p.hq) * p.nq + rh / p.hq] = some ? (mx - float(kFwdExp<T>)) * kLn2 + logf(total) : -INFINITY;
+    p.lse[(rh % p.hq) * p.nq + rh / p.hq] = some ? lse_of<T>(p, mx, total) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
