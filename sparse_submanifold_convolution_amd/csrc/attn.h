@@ -43,7 +43,8 @@ struct Params {
   void *o, *dq, *dk, *dv;
   float* lse;          // [hq][nq]
   float* delta;        // [hq][nq], backward: sum over d of dout * out, as the dQ pass corrects it
-  const uint32_t* bound;  // backward, fp16: bits of max |dout row|^2 and max |v row|^2
+  const float* bound;  // backward, fp16: maxima of |dout row|^2 and |v row|^2, [bounds][2]
+  int32_t bounds;
   const int32_t *qoff, *koff;
   const uint8_t* mask;
   int64_t nq, nk;
@@ -737,33 +738,45 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
 // backward
 // ---------------------------------------------------------------------------
 
-// fp16: the largest |dout row|^2 and |v row|^2 (maxima: any order gives the same), which bound dS for its scaling to
-// fp16's range.  16 lanes a (row, head); infinite or NaN rows are left out and spoil the results they reach.
+// workgroups of bound_kernel: each leaves its two maxima for the passes to reduce
+constexpr int kBoundBlocks = 512;
+
+// fp16: the largest |dout row|^2 and |v row|^2, which bound dS for its scaling to fp16's range; workgroup b's maxima go
+// to bound[2 b], bound[2 b + 1].  16 lanes a (row, head), four rows on their way at a time; infinite or NaN rows are left
+// out and spoil the results they reach.
 template <typename T>
-__global__ void __launch_bounds__(256) bound_kernel(Params p, uint32_t* bound) {
+__global__ void __launch_bounds__(256) bound_kernel(Params p, float* bound) {
+  __shared__ float lq[4], lv[4];
   const int sub = threadIdx.x & 15, chunks = p.d / 8;
   const int64_t nd = p.nq * p.hq, nv = p.nk * p.hk, step = int64_t(gridDim.x) * 16;
   float mq = 0.f, mv = 0.f;
-  const int64_t first = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
   // whole waves iterate together: the groups' sums cross lanes
-  for (int64_t base = int64_t(blockIdx.x) * 16; base < nd + nv; base += step) {
-    const int64_t id = first + (base - int64_t(blockIdx.x) * 16), vi = id - nd;
-    const bool isq = id < nd, isv = !isq && vi < nv && (!p.mask || p.mask[vi / p.hk]);
-    float sq = 0.f;
-    if (isq || isv) {
-      const T* a = isq ? static_cast<const T*>(p.dout) + id * p.d
-                       : static_cast<const T*>(p.v) + vi / p.hk * p.v_row + vi % p.hk * p.v_head;
-      for (int ch = sub; ch < chunks; ch += 16) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(a + ch * 8);
+  for (int64_t base = int64_t(blockIdx.x) * 16; base < nd + nv; base += 4 * step) {
+    bool isq[4], isv[4];
+    u32x4 x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sq = Elt<T>::dot(x[e], x[e], sq);
+    for (int u = 0; u < 4; ++u) {
+      const int64_t id = base + u * step + (threadIdx.x >> 4), vi = id - nd;
+      isq[u] = id < nd;
+      isv[u] = !isq[u] && vi < nv && (!p.mask || p.mask[vi / p.hk]);
+      x[u] = u32x4{0, 0, 0, 0};
+      if ((isq[u] || isv[u]) && sub < chunks) {
+        const T* a = isq[u] ? static_cast<const T*>(p.dout) + id * p.d
+                            : static_cast<const T*>(p.v) + vi / p.hk * p.v_row + vi % p.hk * p.v_head;
+        x[u] = *reinterpret_cast<const u32x4*>(a + sub * 8);
       }
     }
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) sq += __shfl_xor(sq, d);
-    if (sq < INFINITY) {
-      if (isq) mq = fmaxf(mq, sq);
-      if (isv) mv = fmaxf(mv, sq);
+    for (int u = 0; u < 4; ++u) {
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sq = Elt<T>::dot(x[u][e], x[u][e], sq);
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) sq += __shfl_xor(sq, d);
+      if (sq < INFINITY) {
+        if (isq[u]) mq = fmaxf(mq, sq);
+        if (isv[u]) mv = fmaxf(mv, sq);
+      }
     }
   }
 #pragma unroll
@@ -772,15 +785,16 @@ __global__ void __launch_bounds__(256) bound_kernel(Params p, uint32_t* bound) {
     mv = fmaxf(mv, __shfl_xor(mv, d));
   }
   if ((threadIdx.x & 63) == 0) {
-    if (mq > 0.f) atomicMax(&bound[0], __float_as_uint(mq));
-    if (mv > 0.f) atomicMax(&bound[1], __float_as_uint(mv));
+    lq[threadIdx.x >> 6] = mq;
+    lv[threadIdx.x >> 6] = mv;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    bound[2 * blockIdx.x] = fmaxf(fmaxf(lq[0], lq[1]), fmaxf(lq[2], lq[3]));
+    bound[2 * blockIdx.x + 1] = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
   }
 }
-
-// clears the two bounds before the maxima
-static __global__ void bound_clear_kernel(uint32_t* bound) {
-  if (threadIdx.x < 2) bound[threadIdx.x] = 0u;
-}
+static_assert(SSC_MAX_HEAD_DIM <= 16 * 8, "a row is one vector a lane");
 
 // Power of two for dS in fp16: |dS| <= |dP - delta| <= 2 |dout row| |v row| (out lies within the values it averages),
 // so with b2 = max |dout row|^2 max |v row|^2 < 2^e the scaled dS stays below 2^(1 + e/2 + s) <= 2^15.5 < 65504 for
@@ -790,7 +804,17 @@ __device__ __forceinline__ int ds_exp(const Params& p) {
   if constexpr (kPExp<T> == 0) {
     return 0;
   } else {
-    const float b2 = __uint_as_float(p.bound[0]) * __uint_as_float(p.bound[1]);
+    float mq = 0.f, mv = 0.f;
+    for (int i = threadIdx.x & 63; i < p.bounds; i += 64) {
+      mq = fmaxf(mq, p.bound[2 * i]);
+      mv = fmaxf(mv, p.bound[2 * i + 1]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      mq = fmaxf(mq, __shfl_xor(mq, d));
+      mv = fmaxf(mv, __shfl_xor(mv, d));
+    }
+    const float b2 = mq * mv;
     if (!(b2 > 0.f) || !(b2 < INFINITY)) return 0;
     int e;
     (void)frexpf(b2, &e);
@@ -1295,7 +1319,7 @@ struct BwdPlan {
 // the backward pass's regions of the workspace
 struct BwdParts {
   float *q_sum, *q_mean, *q_err, *k_sum, *v_sum;
-  uint32_t* bound;
+  float* bound;
 };
 
 // launches of one element type (defined once per type)
@@ -1400,9 +1424,9 @@ template <typename T>
 int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s) {
   p.bound = w.bound;
   if constexpr (kPExp<T> != 0) {
-    const int64_t blocks = (p.nq * p.hq + p.nk * p.hk + 15) / 16;
-    bound_clear_kernel<<<1, 64, 0, s>>>(w.bound);
-    bound_kernel<T><<<unsigned(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(p, w.bound);
+    const int64_t blocks = (p.nq * p.hq + p.nk * p.hk + 63) / 64;
+    p.bounds = int(blocks < kBoundBlocks ? blocks : kBoundBlocks);
+    if (p.bounds > 0) bound_kernel<T><<<unsigned(p.bounds), 256, 0, s>>>(p, w.bound);
   }
   // dK reads the delta that the dQ pass forms, so that pass runs for either
   if ((p.dq || p.dk) && p.nq > 0) {

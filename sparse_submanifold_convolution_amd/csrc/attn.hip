@@ -102,7 +102,7 @@ Ws ws_layout(const ssc_attn_shape& a, bool backward) {
     }
   } else {
     const BwdPlan b = bwd_plan(a);
-    w.bound = take(256);
+    w.bound = take(size_t(kBoundBlocks) * 8);
     w.delta = take(qn * 4);
     if (b.q_split > 1) {
       w.part_q = take(size_t(b.q_split) * qn * d * 4);
@@ -253,7 +253,7 @@ extern "C" int ssc_cross_attn_bwd(const ssc_attn_shape* shape, const void* q, co
   p.mask = kv_mask;
   const BwdParts parts{reinterpret_cast<float*>(ws + w.part_q), reinterpret_cast<float*>(ws + w.mean_q),
                        reinterpret_cast<float*>(ws + w.err_q),  reinterpret_cast<float*>(ws + w.part_k),
-                       reinterpret_cast<float*>(ws + w.part_v), reinterpret_cast<uint32_t*>(ws + w.bound)};
+                       reinterpret_cast<float*>(ws + w.part_v), reinterpret_cast<float*>(ws + w.bound)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (a.dtype == SSC_F32) return launch_bwd<float>(p, b, parts, s);
