@@ -499,7 +499,9 @@ int ssc_qk_norm_rope_bwd(const ssc_norm_rope_shape* shape, const void* q, const 
  * Offsets must not decrease; they are taken into [0, rows].
  * Scores, statistics and sums are fp32.  Probabilities (and dS) are rounded to
  * `dtype` for the second products; in fp16 they carry a power of two that
- * keeps small ones normal.  Sums run in a fixed order: results repeat.
+ * keeps small ones normal (dS's follows the largest dout and value rows of its
+ * sample and key head).  Sums run in a fixed order: results repeat, and do not
+ * depend on other samples' values or on rows of no sample.
  * ------------------------------------------------------------------------ */
 #define SSC_MAX_HEAD_DIM 128
 #define SSC_MAX_ATTN_BATCH 65536

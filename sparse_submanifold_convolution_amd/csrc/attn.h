@@ -43,8 +43,9 @@ struct Params {
   void *o, *dq, *dk, *dv;
   float* lse;          // [hq][nq]
   float* delta;        // [hq][nq], backward: sum over d of dout * out, as the dQ pass corrects it
-  const float* bound;  // backward, fp16: maxima of |dout row|^2 and |v row|^2, [bounds][2]
-  int32_t bounds;
+  // backward, fp16: maxima of |dout row|^2 and |v row|^2 by key head and piece of rows (see piece_rows)
+  const float *top_q, *top_k;
+  int32_t q_piece, k_piece, q_pieces, k_pieces;  // rows of a piece, pieces
   const int32_t *qoff, *koff;
   const uint8_t* mask;
   int64_t nq, nk;
@@ -299,6 +300,7 @@ struct Segment {
   int64_t other;   // first row of the sample on the other side
   int32_t other_len;
   int32_t tile;    // tile number inside the segment
+  int32_t index;   // of the segment: 0 before the first sample, b + 1 for sample b
 };
 
 // Finds tile t of the concatenated segments, each holding ceil(len * mult / cols) tiles; false past the last.  Each
@@ -331,6 +333,7 @@ __device__ __forceinline__ bool find_segment(const int32_t* off, int64_t n, cons
       seg->tile = t - __builtin_amdgcn_readlane(incl - mine, w);
       seg->other = __builtin_amdgcn_readlane(int(ob), w);
       seg->other_len = __builtin_amdgcn_readlane(olen, w);
+      seg->index = base + w;
       return true;
     }
     t -= total;
@@ -738,32 +741,58 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
 // backward
 // ---------------------------------------------------------------------------
 
-// workgroups of bound_kernel: each leaves its two maxima for the passes to reduce
-constexpr int kBoundBlocks = 512;
+// fp16: dS carries a power of two that keeps it inside the type's range.  It follows the largest |dout row|^2 and
+// |v row|^2 of the sample and key head that dS belongs to, so that a sample's and a head's gradients do not depend on the
+// values of others.  The maxima are formed by pieces: the rows of segment s within block g (`rows` of them) of one side
+// are piece g + s, which numbers the pieces in row order with no table of where a segment's begin, and each piece is one
+// workgroup's per key head.  Numbers that no row has (empty segments leave them) are never written nor read.
+constexpr int kPieceBlocks = 512;  // blocks of a side times key heads, at most: what the rows are spread over
+inline int piece_rows(int64_t rows, int64_t heads_kv, int64_t rows_least) {
+  const int64_t blocks = kPieceBlocks / heads_kv > 0 ? kPieceBlocks / heads_kv : 1, n = (rows + blocks - 1) / blocks;
+  return int(n > rows_least ? n : rows_least);
+}
+inline int piece_count(int64_t rows, int piece, int64_t batch) { return int((rows + piece - 1) / piece + batch + 2); }
 
-// fp16: the largest |dout row|^2 and |v row|^2, which bound dS for its scaling to fp16's range; workgroup b's maxima go
-// to bound[2 b], bound[2 b + 1].  16 lanes a (row, head), four rows on their way at a time; infinite or NaN rows are left
-// out and spoil the results they reach.
+// The maxima of piece blockIdx.x (the query side's first, then the key side's) and key head blockIdx.y.  16 lanes a (row,
+// head), four rows on their way at a time; infinite or NaN rows are left out and spoil the results they reach, masked
+// ones are left out.  Rows of no sample have no maxima.
 template <typename T>
-__global__ void __launch_bounds__(256) bound_kernel(Params p, float* bound) {
-  __shared__ float lq[4], lv[4];
-  const int sub = threadIdx.x & 15, chunks = p.d / 8;
-  const int64_t nd = p.nq * p.hq, nv = p.nk * p.hk, step = int64_t(gridDim.x) * 16;
-  float mq = 0.f, mv = 0.f;
+__global__ void __launch_bounds__(256) top_kernel(Params p, float* top_q, float* top_k) {
+  __shared__ float lmax[4];
+  const int lane = threadIdx.x & 63, sub = threadIdx.x & 15, hk = blockIdx.y, chunks = p.d / 8;
+  const bool isq = int(blockIdx.x) < p.q_pieces;
+  const int piece = isq ? blockIdx.x : blockIdx.x - p.q_pieces, rows = isq ? p.q_piece : p.k_piece;
+  const int32_t* off = isq ? p.qoff : p.koff;
+  const int64_t n = isq ? p.nq : p.nk;
+  // the piece's segment is the last one whose first piece is not past it: each lane looks at one of 64 candidates
+  int seg = 0, end = p.batch + 2;
+  while (end - seg > 1) {
+    const int step = (end - seg + 63) / 64, s = seg + lane * step;
+    const int first = s < end ? (s == 0 ? 0 : int(clamp_off(off, s - 1, n)) / rows + s) : 0x7FFFFFFF;
+    const int k = __popcll(__ballot(first <= piece)) - 1;
+    seg += (k < 0 ? 0 : k) * step;
+    end = seg + step < end ? seg + step : end;
+  }
+  seg = uniform(seg);
+  if (seg == 0 || seg > p.batch) return;
+  const int64_t block = int64_t(piece - seg) * rows, begin = clamp_off(off, seg - 1, n), stop = clamp_off(off, seg, n);
+  const int64_t lo = begin > block ? begin : block, hi = stop < block + rows ? stop : block + rows;
+  if (lo >= hi) return;
+  const int items = int(hi - lo) * (isq ? p.G : 1);
+  float most = 0.f;
   // whole waves iterate together: the groups' sums cross lanes
-  for (int64_t base = int64_t(blockIdx.x) * 16; base < nd + nv; base += 4 * step) {
-    bool isq[4], isv[4];
+  for (int base = 0; base < items; base += 4 * 16) {
     u32x4 x[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t id = base + u * step + (threadIdx.x >> 4), vi = id - nd;
-      isq[u] = id < nd;
-      isv[u] = !isq[u] && vi < nv && (!p.mask || p.mask[vi / p.hk]);
+      const int i = base + u * 16 + int(threadIdx.x >> 4);
       x[u] = u32x4{0, 0, 0, 0};
-      if ((isq[u] || isv[u]) && sub < chunks) {
-        const T* a = isq[u] ? static_cast<const T*>(p.dout) + id * p.d
-                            : static_cast<const T*>(p.v) + vi / p.hk * p.v_row + vi % p.hk * p.v_head;
-        x[u] = *reinterpret_cast<const u32x4*>(a + sub * 8);
+      if (i < items && sub < chunks) {
+        const int tok = isq ? int(div_g(uint32_t(i), p)) : i;
+        const int64_t row = lo + tok;
+        const T* a = isq ? static_cast<const T*>(p.dout) + (row * p.hq + hk * p.G + (i - tok * p.G)) * p.d
+                         : static_cast<const T*>(p.v) + row * p.v_row + hk * p.v_head;
+        if (isq || !p.mask || p.mask[row]) x[u] = *reinterpret_cast<const u32x4*>(a + sub * 8);
       }
     }
 #pragma unroll
@@ -773,48 +802,42 @@ __global__ void __launch_bounds__(256) bound_kernel(Params p, float* bound) {
       for (int e = 0; e < 4; ++e) sq = Elt<T>::dot(x[u][e], x[u][e], sq);
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) sq += __shfl_xor(sq, d);
-      if (sq < INFINITY) {
-        if (isq[u]) mq = fmaxf(mq, sq);
-        if (isv[u]) mv = fmaxf(mv, sq);
-      }
+      if (sq < INFINITY) most = fmaxf(most, sq);
     }
   }
 #pragma unroll
-  for (int d = 16; d < 64; d <<= 1) {
-    mq = fmaxf(mq, __shfl_xor(mq, d));
-    mv = fmaxf(mv, __shfl_xor(mv, d));
-  }
-  if ((threadIdx.x & 63) == 0) {
-    lq[threadIdx.x >> 6] = mq;
-    lv[threadIdx.x >> 6] = mv;
-  }
+  for (int d = 16; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+  if (lane == 0) lmax[threadIdx.x >> 6] = most;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    bound[2 * blockIdx.x] = fmaxf(fmaxf(lq[0], lq[1]), fmaxf(lq[2], lq[3]));
-    bound[2 * blockIdx.x + 1] = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
-  }
+  if (threadIdx.x == 0)
+    (isq ? top_q + int64_t(hk) * p.q_pieces : top_k + int64_t(hk) * p.k_pieces)[piece] =
+        fmaxf(fmaxf(lmax[0], lmax[1]), fmaxf(lmax[2], lmax[3]));
 }
 static_assert(SSC_MAX_HEAD_DIM <= 16 * 8, "a row is one vector a lane");
 
-// Power of two for dS in fp16: |dS| <= |dP - delta| <= 2 |dout row| |v row| (out lies within the values it averages),
-// so with b2 = max |dout row|^2 max |v row|^2 < 2^e the scaled dS stays below 2^(1 + e/2 + s) <= 2^15.5 < 65504 for
-// s = 14 - floor(e / 2).  The rest of fp16's range (steps of 2^-24) is then all below the largest possible entry.
+// the largest of the pieces of rows [begin, begin + len) of segment `index`
+__device__ __forceinline__ float top_of(const float* top, int rows, int64_t begin, int len, int index) {
+  const int last = int((begin + len - 1) / rows) + index;
+  float m = 0.f;
+  for (int i = int(begin / rows) + index + int(threadIdx.x & 63); i <= last; i += 64) m = fmaxf(m, top[i]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  return m;
+}
+
+// Power of two for dS in fp16 of one sample and key head (q: the sample's query rows, k: its key rows): |dS| <=
+// |dP - delta| <= 2 |dout row| |v row| (out lies within the values it averages), so with b2 = max |dout row|^2
+// max |v row|^2 < 2^e the scaled dS stays below 2^(1 + e/2 + s) <= 2^15.5 < 65504 for s = 14 - floor(e / 2).  The rest of
+// fp16's range (steps of 2^-24) is then all below the largest possible entry.
 template <typename T>
-__device__ __forceinline__ int ds_exp(const Params& p) {
+__device__ __forceinline__ int ds_exp(const Params& p, int hk, int index, int64_t q_begin, int q_len, int64_t k_begin,
+                                      int k_len) {
   if constexpr (kPExp<T> == 0) {
     return 0;
   } else {
-    float mq = 0.f, mv = 0.f;
-    for (int i = threadIdx.x & 63; i < p.bounds; i += 64) {
-      mq = fmaxf(mq, p.bound[2 * i]);
-      mv = fmaxf(mv, p.bound[2 * i + 1]);
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      mq = fmaxf(mq, __shfl_xor(mq, d));
-      mv = fmaxf(mv, __shfl_xor(mv, d));
-    }
-    const float b2 = mq * mv;
+    if (q_len <= 0 || k_len <= 0) return 0;  // nothing attends
+    const float b2 = top_of(p.top_q + int64_t(hk) * p.q_pieces, p.q_piece, q_begin, q_len, index) *
+                     top_of(p.top_k + int64_t(hk) * p.k_pieces, p.k_piece, k_begin, k_len, index);
     if (!(b2 > 0.f) || !(b2 < INFINITY)) return 0;
     int e;
     (void)frexpf(b2, &e);
@@ -858,7 +881,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_
   const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
   const int dchunks = p.d / TL::kVec;
   const float c = p.scale * kLog2e;
-  const int dse = ds_exp<T>(p);
+  const int dse = ds_exp<T>(p, hk, sg.index, sg.begin, sg.len, sg.other, sg.other_len);
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);  // probabilities carry 2^kPExp
 
   u32x4 qf[TL::kFrags], df[TL::kFrags];
@@ -1146,7 +1169,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
   const int dchunks = p.d / TL::kVec;
   const float c = p.scale * kLog2e;
-  const int dse = ds_exp<T>(p);
+  const int dse = DK ? ds_exp<T>(p, hk, sg.index, sg.other, sg.other_len, sg.begin, sg.len) : 0;
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);
 
   const int col = sg.tile * TC + wave * 32 + (lane & 31);
@@ -1319,7 +1342,7 @@ struct BwdPlan {
 // the backward pass's regions of the workspace
 struct BwdParts {
   float *q_sum, *q_mean, *q_err, *k_sum, *v_sum;
-  float* bound;
+  float *top_q, *top_k;
 };
 
 // launches of one element type (defined once per type)
@@ -1422,11 +1445,11 @@ int launch_fwd_impl(const Params& p, const FwdPlan& f, hipStream_t s) {
 
 template <typename T>
 int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s) {
-  p.bound = w.bound;
   if constexpr (kPExp<T> != 0) {
-    const int64_t blocks = (p.nq * p.hq + p.nk * p.hk + 63) / 64;
-    p.bounds = int(blocks < kBoundBlocks ? blocks : kBoundBlocks);
-    if (p.bounds > 0) bound_kernel<T><<<unsigned(p.bounds), 256, 0, s>>>(p, w.bound);
+    p.top_q = w.top_q;
+    p.top_k = w.top_k;
+    if ((p.dq || p.dk) && p.nq > 0 && p.nk > 0)
+      top_kernel<T><<<dim3(unsigned(p.q_pieces + p.k_pieces), unsigned(p.hk)), 256, 0, s>>>(p, w.top_q, w.top_k);
   }
   // dK reads the delta that the dQ pass forms, so that pass runs for either
   if ((p.dq || p.dk) && p.nq > 0) {

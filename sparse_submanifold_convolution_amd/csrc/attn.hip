@@ -81,8 +81,36 @@ BwdPlan bwd_plan(const ssc_attn_shape& a) {
   return b;
 }
 
+Params base_params(const ssc_attn_shape& a) {
+  Params p{};
+  p.nq = a.nq;
+  p.nk = a.nk;
+  p.q_row = a.q_row_stride;
+  p.q_head = a.q_head_stride;
+  p.k_row = a.k_row_stride;
+  p.k_head = a.k_head_stride;
+  p.v_row = a.v_row_stride;
+  p.v_head = a.v_head_stride;
+  p.batch = a.batch;
+  p.hq = a.heads_q;
+  p.hk = a.heads_kv;
+  p.d = a.head_dim;
+  p.G = a.heads_q / a.heads_kv;
+  int l = 0;
+  while ((1 << l) < p.G) ++l;
+  p.gmul = uint32_t((uint64_t(1) << (31 + l)) / uint64_t(p.G) + 1);
+  p.gshift = 31 + l;
+  p.scale = a.scale;
+  // a piece's workgroup has four rows on their way for each of its 16 groups of lanes
+  p.q_piece = piece_rows(a.nq, a.heads_kv, 64 / p.G > 0 ? 64 / p.G : 1);
+  p.k_piece = piece_rows(a.nk, a.heads_kv, 64);
+  p.q_pieces = piece_count(a.nq, p.q_piece, a.batch);
+  p.k_pieces = piece_count(a.nk, p.k_piece, a.batch);
+  return p;
+}
+
 struct Ws {
-  size_t part_q = 0, mean_q = 0, err_q = 0, part_k = 0, part_v = 0, delta = 0, bound = 0, total = 0;
+  size_t part_q = 0, mean_q = 0, err_q = 0, part_k = 0, part_v = 0, delta = 0, top_q = 0, top_k = 0, total = 0;
 };
 
 Ws ws_layout(const ssc_attn_shape& a, bool backward) {
@@ -102,7 +130,11 @@ Ws ws_layout(const ssc_attn_shape& a, bool backward) {
     }
   } else {
     const BwdPlan b = bwd_plan(a);
-    w.bound = take(size_t(kBoundBlocks) * 8);
+    if (a.dtype == SSC_F16) {
+      const Params p = base_params(a);
+      w.top_q = take(size_t(p.q_pieces) * size_t(a.heads_kv) * 4);
+      w.top_k = take(size_t(p.k_pieces) * size_t(a.heads_kv) * 4);
+    }
     w.delta = take(qn * 4);
     if (b.q_split > 1) {
       w.part_q = take(size_t(b.q_split) * qn * d * 4);
@@ -146,29 +178,6 @@ int check_shape(const ssc_attn_shape* a) {
       int64_t(b.k_tiles) * a->heads_kv * b.k_split > lim)
     return SSC_ERR_UNSUPPORTED;
   return SSC_OK;
-}
-
-Params base_params(const ssc_attn_shape& a) {
-  Params p{};
-  p.nq = a.nq;
-  p.nk = a.nk;
-  p.q_row = a.q_row_stride;
-  p.q_head = a.q_head_stride;
-  p.k_row = a.k_row_stride;
-  p.k_head = a.k_head_stride;
-  p.v_row = a.v_row_stride;
-  p.v_head = a.v_head_stride;
-  p.batch = a.batch;
-  p.hq = a.heads_q;
-  p.hk = a.heads_kv;
-  p.d = a.head_dim;
-  p.G = a.heads_q / a.heads_kv;
-  int l = 0;
-  while ((1 << l) < p.G) ++l;
-  p.gmul = uint32_t((uint64_t(1) << (31 + l)) / uint64_t(p.G) + 1);
-  p.gshift = 31 + l;
-  p.scale = a.scale;
-  return p;
 }
 
 bool bad(const void* ptr) { return !ptr || !aligned16(ptr); }
@@ -253,7 +262,8 @@ extern "C" int ssc_cross_attn_bwd(const ssc_attn_shape* shape, const void* q, co
   p.mask = kv_mask;
   const BwdParts parts{reinterpret_cast<float*>(ws + w.part_q), reinterpret_cast<float*>(ws + w.mean_q),
                        reinterpret_cast<float*>(ws + w.err_q),  reinterpret_cast<float*>(ws + w.part_k),
-                       reinterpret_cast<float*>(ws + w.part_v), reinterpret_cast<float*>(ws + w.bound)};
+                       reinterpret_cast<float*>(ws + w.part_v), reinterpret_cast<float*>(ws + w.top_q),
+                       reinterpret_cast<float*>(ws + w.top_k)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (a.dtype == SSC_F32) return launch_bwd<float>(p, b, parts, s);
