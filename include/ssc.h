@@ -438,7 +438,8 @@ enum ssc_rope_layout {
  * elements, multiples of 16 bytes, not negative; a head's elements are
  * contiguous, so the heads may be views of one packed projection. */
 typedef struct ssc_norm_rope_shape {
-  int64_t n;                             /* rows, at most SSC_MAX_ATTN_ROWS */
+  int64_t n;                             /* rows, at most SSC_MAX_ATTN_ROWS; every 8 heads of a row take a lane (4
+                                          * lanes at least) per 16 bytes of a head, fewer than 2^32 in all */
   int64_t q_row_stride, q_head_stride;
   int64_t k_row_stride, k_head_stride;
   int64_t pos_row_stride;                /* int32s from one row of positions to the next */
@@ -511,7 +512,10 @@ int ssc_qk_norm_rope_bwd(const ssc_norm_rope_shape* shape, const void* q, const 
 
 /* Sizes of a call (a host struct, read during the call).  Strides as in
  * ssc_norm_rope_shape, row strides at most SSC_MAX_ATTN_ROW_STRIDE elements; 0
- * is allowed (a broadcast input). */
+ * is allowed (a broadcast input).  A pass has rows / tile + batch + 2 tiles of
+ * 128 rows (256 in the forward pass of 16-bit heads of over 96, 32 where the
+ * samples have no more query rows on average), each two threads a row and key
+ * head (eight for 32), and has to stay below 2^32 threads. */
 typedef struct ssc_attn_shape {
   int64_t nq, nk;                        /* rows, each at most SSC_MAX_ATTN_ROWS; nq * heads_q / heads_kv <= 2^30 */
   int64_t q_row_stride, q_head_stride;

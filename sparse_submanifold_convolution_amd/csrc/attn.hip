@@ -152,6 +152,11 @@ Ws ws_layout(const ssc_attn_shape& a, bool backward) {
   return w;
 }
 
+// whether a pass of `waves` waves a workgroup fits a launch: HIP takes fewer than 2^32 threads in a dimension
+bool launches(int64_t tiles, int64_t nsplit, int64_t waves, const ssc_attn_shape& a) {
+  return ceil_div(tiles * a.heads_kv * nsplit, 8) * 8 * waves * 64 < (1LL << 32);
+}
+
 int check_shape(const ssc_attn_shape* a) {
   if (!a) return SSC_ERR_INVALID_ARG;
   if (a->dtype != SSC_F32 && a->dtype != SSC_F16 && a->dtype != SSC_BF16) return SSC_ERR_UNSUPPORTED;
@@ -173,9 +178,10 @@ int check_shape(const ssc_attn_shape* a) {
     if (v < 0 || v > (1LL << 40) || (v * e) % 16 != 0) return SSC_ERR_INVALID_ARG;
   const FwdPlan f = fwd_plan(*a);
   const BwdPlan b = bwd_plan(*a);
-  const int64_t lim = 1LL << 30;
-  if (int64_t(f.tiles) * a->heads_kv * f.nsplit > lim || int64_t(b.q_tiles) * a->heads_kv * b.q_split > lim ||
-      int64_t(b.k_tiles) * a->heads_kv * b.k_split > lim)
+  // The joins and the sums of splits run only where the rows' workgroups do not fill the chip, far below the limit, and
+  // the pieces of top_kernel number at most 2 (kPieceBlocks + batch + 3).
+  if (!launches(f.tiles, f.nsplit, f.few ? 4 : fwd_waves(esize(a->dtype), a->head_dim > 96 ? 128 : 96), *a) ||
+      !launches(b.q_tiles, b.q_split, 4, *a) || !launches(b.k_tiles, b.k_split, 4, *a))
     return SSC_ERR_UNSUPPORTED;
   return SSC_OK;
 }

@@ -351,6 +351,16 @@ int lanes_of(const ssc_norm_rope_shape& a) {
   return l;
 }
 
+// Groups that share a row's heads in the forward pass: a group walks up to 8 (the angles are then a small part of its
+// work), fewer when the rows alone do not give the chip 4096 waves (22.4k rows x 8 heads: 14.7 us with twice as many,
+// 13.4 us)
+int64_t fwd_chunks(const ssc_norm_rope_shape& a) {
+  const int64_t heads = a.heads_q + a.heads_kv;
+  int64_t chunks = (heads + 7) / 8;
+  while (chunks < heads && a.n * chunks * lanes_of(a) < 262144) chunks *= 2;
+  return chunks > heads ? heads : chunks;
+}
+
 // row blocks of the backward grid: enough workgroups to fill the chip, no more than the rows need
 int64_t row_blocks(const ssc_norm_rope_shape& a) {
   const int64_t ny = (a.heads_q + a.heads_kv + kRopeHeads - 1) / kRopeHeads;
@@ -373,8 +383,8 @@ int rope_check(const ssc_norm_rope_shape* a) {
   if (a->layout != SSC_ROPE_INTERLEAVED && a->layout != SSC_ROPE_HALVES) return SSC_ERR_UNSUPPORTED;
   if (a->layout == SSC_ROPE_HALVES && a->pairs % vec != 0) return SSC_ERR_UNSUPPORTED;
   if (a->norm && !(a->eps >= 0.f && a->eps < INFINITY)) return SSC_ERR_INVALID_ARG;
-  // groups of up to 64 lanes, at least one for every eight heads of a row, in workgroups of 256
-  if (a->n * ((a->heads_q + a->heads_kv + 7) / 8) / 4 >= (1LL << 31) - 1) return SSC_ERR_UNSUPPORTED;
+  // HIP takes fewer than 2^32 threads in a dimension of a launch
+  if ((a->n * fwd_chunks(*a) * lanes_of(*a) + 255) / 256 * 256 >= (1LL << 32)) return SSC_ERR_UNSUPPORTED;
   const int64_t st[4] = {a->q_row_stride, a->q_head_stride, a->k_row_stride, a->k_head_stride};
   for (int64_t v : st)
     if (v < 0 || v > (1LL << 40) || v % vec != 0) return SSC_ERR_INVALID_ARG;
@@ -401,14 +411,8 @@ RopeParams rope_params(const ssc_norm_rope_shape& a) {
 
 template <typename T, int L, bool HALVES>
 void fwd_lanes(const ssc_norm_rope_shape& a, RopeParams& p, hipStream_t s) {
-  const int heads = a.heads_q + a.heads_kv;
-  // Heads a group walks: up to 8 (the angles are then a small part of its work), fewer when the rows alone do not
-  // give the chip 4096 waves (22.4k rows x 8 heads: 14.7 us with twice as many, 13.4 us)
-  int64_t chunks = (heads + 7) / 8;
-  while (chunks < heads && a.n * chunks * L < 262144) chunks *= 2;
-  if (chunks > heads) chunks = heads;
-  p.chunks = int32_t(chunks);
-  const int64_t threads = a.n * chunks * L;
+  p.chunks = int32_t(fwd_chunks(a));
+  const int64_t threads = a.n * p.chunks * L;
   const unsigned grid = unsigned((threads + 255) / 256);
   if (a.norm)
     rope_fwd<T, L, HALVES, true><<<grid, 256, 0, s>>>(p);
