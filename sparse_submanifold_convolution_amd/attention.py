@@ -56,15 +56,26 @@ def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device,
     return rows, heads, dim, rs, hs
 
 
-def _aligned(t: torch.Tensor) -> bool:
+_MAX_ROW_STRIDE = 1 << 23  # SSC_MAX_ATTN_ROW_STRIDE
+
+
+def _taken(t: torch.Tensor, most_row: int) -> bool:
     e = t.element_size()
-    return (t.stride(2) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) * e % 16 == 0)
+    return (t.stride(2) == 1 and t.data_ptr() % 16 == 0
+            and (t.shape[0] <= 1 or t.stride(0) * e % 16 == 0 and t.stride(0) <= most_row)
             and (t.shape[1] <= 1 or t.stride(1) * e % 16 == 0))
 
 
-def _dense(t: torch.Tensor) -> torch.Tensor:
-    """t itself where the calls take its strides, else a contiguous copy."""
-    return t if t.dim() != 3 or _aligned(t) else t.contiguous()
+def _dense(t: torch.Tensor, most_row: int = 1 << 40) -> torch.Tensor:
+    """t itself where the calls take its strides and its address, else a contiguous copy."""
+    return t if t.dim() != 3 or _taken(t, most_row) else t.clone(memory_format=torch.contiguous_format)
+
+
+def _packed(t: torch.Tensor | None) -> torch.Tensor | None:
+    """t contiguous and 16-byte aligned: a contiguous view may start anywhere in its buffer."""
+    if t is None or t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 # ---------------------------------------------------------------------------
@@ -186,6 +197,7 @@ class QKNormRopeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, positions, table, eps, norm, layout):
         q, k = (None if t is None else _dense(t) for t in (q, k))
+        q_weight, k_weight = _packed(q_weight), _packed(k_weight)
         ctx.save_for_backward(q, k, q_weight, k_weight, positions)
         ctx.rest = (table, eps, norm, layout)
         return qk_norm_rope_fwd(q, k, positions, table, q_weight, k_weight, eps, norm, layout)
@@ -195,8 +207,8 @@ class QKNormRopeFunction(torch.autograd.Function):
         q, k, qw, kw, positions = ctx.saved_tensors
         table, eps, norm, layout = ctx.rest
         need = ctx.needs_input_grad
-        dqo = dqo.contiguous() if dqo is not None and q is not None and (need[0] or need[2]) else None
-        dko = dko.contiguous() if dko is not None and k is not None and (need[1] or need[3]) else None
+        dqo = _packed(dqo) if dqo is not None and q is not None and (need[0] or need[2]) else None
+        dko = _packed(dko) if dko is not None and k is not None and (need[1] or need[3]) else None
         if dqo is None and dko is None:
             return (None,) * 9
         dq, dk, dqw, dkw = qk_norm_rope_bwd(q, k, positions, table, dqo, dko, qw, kw, eps, norm, layout,
@@ -300,7 +312,7 @@ class CrossAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, q_offsets, kv_offsets, kv_mask, scale):
-        q, k, v = _dense(q), _dense(k), _dense(v)
+        q, k, v = (_dense(t, _MAX_ROW_STRIDE) for t in (q, k, v))
         out, lse = cross_attention_fwd(q, k, v, q_offsets, kv_offsets, kv_mask, scale)
         ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets, kv_mask)
         ctx.scale = scale
@@ -310,7 +322,7 @@ class CrossAttentionFunction(torch.autograd.Function):
     def backward(ctx, dout):
         q, k, v, out, lse, qo, ko, mask = ctx.saved_tensors
         nq, nk, nv = ctx.needs_input_grad[:3]
-        dq, dk, dv = cross_attention_bwd(q, k, v, out, lse, dout.contiguous(), qo, ko, mask, ctx.scale, nq, nk, nv)
+        dq, dk, dv = cross_attention_bwd(q, k, v, out, lse, _packed(dout), qo, ko, mask, ctx.scale, nq, nk, nv)
         return dq, dk, dv, None, None, None, None
 
 
