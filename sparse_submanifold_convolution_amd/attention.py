@@ -10,6 +10,7 @@ import math
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import DTYPE_CODE, SSCError, _check, _need, lib
 
@@ -203,6 +204,7 @@ class QKNormRopeFunction(torch.autograd.Function):
         return qk_norm_rope_fwd(q, k, positions, table, q_weight, k_weight, eps, norm, layout)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dqo, dko):
         q, k, qw, kw, positions = ctx.saved_tensors
         table, eps, norm, layout = ctx.rest
@@ -319,6 +321,7 @@ class CrossAttentionFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, qo, ko, mask = ctx.saved_tensors
         nq, nk, nv = ctx.needs_input_grad[:3]

@@ -11,6 +11,7 @@ import dataclasses
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssc.so")
 _lib = None
@@ -276,6 +277,7 @@ class SubmConv3dFunction(torch.autograd.Function):
                                None if bias is None else bias.contiguous())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         feats, weight = ctx.saved_tensors
         dX, dW, db = subm_conv3d_bwd(ctx.plan, feats, weight, dout.contiguous(),
@@ -447,6 +449,7 @@ class SparseConv3dFunction(torch.autograd.Function):
                                  None if bias is None else bias.contiguous())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         feats, weight = ctx.saved_tensors
         dX, dW, db = sparse_conv3d_bwd(ctx.plan, feats, weight, dout.contiguous(),
@@ -578,6 +581,7 @@ class GridSampleFunction(torch.autograd.Function):
         return grid_sample_fwd(plan, feats.contiguous(), points.contiguous())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         (points,) = ctx.saved_tensors
         d = grid_sample_bwd(ctx.plan, points, dout.contiguous()) if ctx.needs_input_grad[0] else None
