@@ -12,7 +12,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import DTYPE_CODE, SSCError, _check, _need, lib
+from .binding import DTYPE_CODE, SSCError, _check, _need, _on, lib
 
 ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
 
@@ -158,9 +158,10 @@ def qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None, positions: 
     sh, dev, *_ = _rope_shape(q, k, positions, table, q_weight, k_weight, eps, norm, layout)
     qo = _new(q) if q is not None else None
     ko = _new(k) if k is not None else None
-    _check("ssc_qk_norm_rope_fwd",
-           lib().ssc_qk_norm_rope_fwd(sh, _ptr(q), _ptr(k), *_table_ptrs(positions, table),
-                                      _ptr(q_weight), _ptr(k_weight), _ptr(qo), _ptr(ko), _stream(dev)))
+    with _on(dev):
+        _check("ssc_qk_norm_rope_fwd",
+               lib().ssc_qk_norm_rope_fwd(sh, _ptr(q), _ptr(k), *_table_ptrs(positions, table),
+                                          _ptr(q_weight), _ptr(k_weight), _ptr(qo), _ptr(ko), _stream(dev)))
     return qo, ko
 
 
@@ -185,10 +186,11 @@ def qk_norm_rope_bwd(q: torch.Tensor | None, k: torch.Tensor | None, positions: 
         if nbytes == 0:
             raise SSCError("ssc_qk_norm_rope_workspace_bytes", 2)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check("ssc_qk_norm_rope_bwd",
-           lib().ssc_qk_norm_rope_bwd(sh, _ptr(q), _ptr(k), *_table_ptrs(positions, table), _ptr(q_weight),
-                                      _ptr(k_weight), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dqw),
-                                      _ptr(dkw), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_qk_norm_rope_bwd",
+               lib().ssc_qk_norm_rope_bwd(sh, _ptr(q), _ptr(k), *_table_ptrs(positions, table), _ptr(q_weight),
+                                          _ptr(k_weight), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dqw),
+                                          _ptr(dkw), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
     return dq, dk, dqw, dkw
 
 
@@ -283,9 +285,10 @@ def cross_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     ws = _attn_workspace(sh, 0, dev)
     out = _new(q)
     lse = q.new_empty(rows, dtype=torch.float32)
-    _check("ssc_cross_attn_fwd",
-           lib().ssc_cross_attn_fwd(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(q_offsets), _ptr(kv_offsets),
-                                    _ptr(kv_mask), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_cross_attn_fwd",
+               lib().ssc_cross_attn_fwd(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(q_offsets), _ptr(kv_offsets),
+                                        _ptr(kv_mask), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev)))
     return out, lse
 
 
@@ -302,10 +305,11 @@ def cross_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
     dq = torch.empty_like(dout) if need_dq else None
     dk = _new(k) if need_dk else None
     dv = _new(v) if need_dv else None
-    _check("ssc_cross_attn_bwd",
-           lib().ssc_cross_attn_bwd(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                                    _ptr(q_offsets), _ptr(kv_offsets), _ptr(kv_mask), _ptr(dq), _ptr(dk), _ptr(dv),
-                                    _ptr(ws), ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_cross_attn_bwd",
+               lib().ssc_cross_attn_bwd(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                        _ptr(q_offsets), _ptr(kv_offsets), _ptr(kv_mask), _ptr(dq), _ptr(dk), _ptr(dv),
+                                        _ptr(ws), ws.numel(), _stream(dev)))
     return dq, dk, dv
 
 

@@ -6,6 +6,7 @@ to another implementation.  If libssc.so is missing the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -111,6 +112,16 @@ def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Makes `device` the current GPU: a default stream's handle names none, and work on it goes to the current one."""
+    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
+        return _HERE
+    return torch.cuda.device(device)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> None:
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, "
@@ -153,9 +164,10 @@ def build_neighbor_map(coords: torch.Tensor, shape, key_bits: int = 0, check: bo
     nmap = torch.empty((n, 27), dtype=torch.int32, device=dev)
     perm = torch.empty((n,), dtype=torch.int32, device=dev)
     B, X, Y, Z = (int(s) for s in shape)
-    _check("ssc_build_neighbor_map",
-           lib().ssc_build_neighbor_map(_ptr(coords), n, B, X, Y, Z, int(key_bits), _ptr(nmap), _ptr(perm),
-                                        _ptr(buf), nbytes, _stream(dev)))
+    with _on(dev):
+        _check("ssc_build_neighbor_map",
+               lib().ssc_build_neighbor_map(_ptr(coords), n, B, X, Y, Z, int(key_bits), _ptr(nmap), _ptr(perm),
+                                            _ptr(buf), nbytes, _stream(dev)))
     plan = Plan(nmap, perm, buf, n, tuple(int(s) for s in shape), int(key_bits))
     if check:
         st = plan_status(plan)
@@ -166,20 +178,23 @@ def build_neighbor_map(coords: torch.Tensor, shape, key_bits: int = 0, check: bo
 
 def plan_status(plan: Plan) -> int:
     out = ctypes.c_int32(-1)
-    _check("ssc_plan_status", lib().ssc_plan_status(_ptr(plan.buf), _stream(plan.device), ctypes.byref(out)))
+    with _on(plan.device):
+        _check("ssc_plan_status", lib().ssc_plan_status(_ptr(plan.buf), _stream(plan.device), ctypes.byref(out)))
     return int(out.value)
 
 
 def plan_pair_counts(plan: Plan) -> list[int]:
     arr = (ctypes.c_int64 * 27)()
-    _check("ssc_plan_pair_counts", lib().ssc_plan_pair_counts(_ptr(plan.buf), _stream(plan.device), arr))
+    with _on(plan.device):
+        _check("ssc_plan_pair_counts", lib().ssc_plan_pair_counts(_ptr(plan.buf), _stream(plan.device), arr))
     return [int(v) for v in arr]
 
 
 def plan_row_orders(plan: Plan) -> tuple[int, int, int]:
     """(row orders the GEMMs use: 1 or 3, the first order's 32-row group sum, the valid pairs)."""
     arr = (ctypes.c_int64 * 3)()
-    _check("ssc_plan_row_orders", lib().ssc_plan_row_orders(_ptr(plan.buf), _stream(plan.device), arr))
+    with _on(plan.device):
+        _check("ssc_plan_row_orders", lib().ssc_plan_row_orders(_ptr(plan.buf), _stream(plan.device), arr))
     return int(arr[0]), int(arr[1]), int(arr[2])
 
 
@@ -213,10 +228,11 @@ def subm_conv3d_fwd(plan: Plan, feats: torch.Tensor, weight: torch.Tensor, bias:
         ws = workspace(plan, ci, co, dt)
     if dt not in DTYPE_CODE:
         raise SSCError("ssc_subm_conv3d_fwd", 2)
-    _check("ssc_subm_conv3d_fwd",
-           lib().ssc_subm_conv3d_fwd(_ptr(plan.buf), _ptr(plan.nmap), _ptr(plan.perm), n, ci, co, DTYPE_CODE[dt],
-                                     _ptr(feats), _ptr(weight), _ptr(bias), _ptr(out), _ptr(ws), ws.numel(),
-                                     _stream(dev)))
+    with _on(dev):
+        _check("ssc_subm_conv3d_fwd",
+               lib().ssc_subm_conv3d_fwd(_ptr(plan.buf), _ptr(plan.nmap), _ptr(plan.perm), n, ci, co, DTYPE_CODE[dt],
+                                         _ptr(feats), _ptr(weight), _ptr(bias), _ptr(out), _ptr(ws), ws.numel(),
+                                         _stream(dev)))
     return out
 
 
@@ -234,10 +250,11 @@ def subm_conv3d_fwd_noalloc(plan: Plan, feats: torch.Tensor, weight: torch.Tenso
     if out is None:
         out = torch.empty((n, co), dtype=dt, device=dev)
     _need(out, "out", dt, (n, co), dev)
-    _check("ssc_subm_conv3d_fwd_noalloc",
-           lib().ssc_subm_conv3d_fwd_noalloc(_ptr(plan.buf), _ptr(plan.nmap), _ptr(plan.perm), n, ci, co,
-                                             DTYPE_CODE[dt], _ptr(feats), _ptr(weight), _ptr(bias), _ptr(out),
-                                             _stream(dev)))
+    with _on(dev):
+        _check("ssc_subm_conv3d_fwd_noalloc",
+               lib().ssc_subm_conv3d_fwd_noalloc(_ptr(plan.buf), _ptr(plan.nmap), _ptr(plan.perm), n, ci, co,
+                                                 DTYPE_CODE[dt], _ptr(feats), _ptr(weight), _ptr(bias), _ptr(out),
+                                                 _stream(dev)))
     return out
 
 
@@ -258,10 +275,11 @@ def subm_conv3d_bwd(plan: Plan, feats: torch.Tensor, weight: torch.Tensor, dout:
         db = torch.empty((co,), dtype=dt, device=dev) if need_dbias else None
     if ws is None:
         ws = workspace(plan, ci, co, dt)
-    _check("ssc_subm_conv3d_bwd",
-           lib().ssc_subm_conv3d_bwd(_ptr(plan.buf), _ptr(plan.nmap), _ptr(plan.perm), n, ci, co, DTYPE_CODE[dt],
-                                     _ptr(feats), _ptr(weight), _ptr(dout), _ptr(dX), _ptr(dW), _ptr(db),
-                                     _ptr(ws), ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_subm_conv3d_bwd",
+               lib().ssc_subm_conv3d_bwd(_ptr(plan.buf), _ptr(plan.nmap), _ptr(plan.perm), n, ci, co, DTYPE_CODE[dt],
+                                         _ptr(feats), _ptr(weight), _ptr(dout), _ptr(dX), _ptr(dW), _ptr(db),
+                                         _ptr(ws), ws.numel(), _stream(dev)))
     return dX, dW, db
 
 
@@ -334,14 +352,16 @@ def sparse_out_coords(coords: torch.Tensor, shape, ks: int, stride: int, pad: in
         raise SSCError("ssc_sparse_out_workspace_bytes", 1)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     count = torch.empty(1, dtype=torch.int64, device=dev)
-    _check("ssc_sparse_out_count", lib().ssc_sparse_out_count(_ptr(coords), n, B, X, Y, Z, *geo, _ptr(ws), nbytes,
-                                                              _ptr(count), _stream(dev)))
+    with _on(dev):
+        _check("ssc_sparse_out_count", lib().ssc_sparse_out_count(_ptr(coords), n, B, X, Y, Z, *geo, _ptr(ws), nbytes,
+                                                                  _ptr(count), _stream(dev)))
     n_out = int(count.item())
     if n_out < 0:
         raise SSCError("ssc_sparse_out_count (device)", 5)
     out = torch.empty((n_out, 4), dtype=torch.int32, device=dev)
-    _check("ssc_sparse_out_coords", lib().ssc_sparse_out_coords(_ptr(ws), nbytes, B, X, Y, Z, *geo, _ptr(out),
-                                                                n_out, _stream(dev)))
+    with _on(dev):
+        _check("ssc_sparse_out_coords", lib().ssc_sparse_out_coords(_ptr(ws), nbytes, B, X, Y, Z, *geo, _ptr(out),
+                                                                    n_out, _stream(dev)))
     return out
 
 
@@ -364,9 +384,10 @@ def build_sparse_map(coords: torch.Tensor, shape, ks: int, stride: int, pad: int
     buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     nmap = torch.empty((n_out, 27), dtype=torch.int32, device=dev)
     perm = torch.empty((n_out,), dtype=torch.int32, device=dev)
-    _check("ssc_build_sparse_map",
-           lib().ssc_build_sparse_map(_ptr(coords), n_in, B, X, Y, Z, _ptr(out_coords), n_out, *geo, int(key_bits),
-                                      _ptr(nmap), _ptr(perm), _ptr(buf), nbytes, _stream(dev)))
+    with _on(dev):
+        _check("ssc_build_sparse_map",
+               lib().ssc_build_sparse_map(_ptr(coords), n_in, B, X, Y, Z, _ptr(out_coords), n_out, *geo, int(key_bits),
+                                          _ptr(nmap), _ptr(perm), _ptr(buf), nbytes, _stream(dev)))
     plan = SparsePlan(out_coords, nmap, perm, buf, n_in, n_out, (B, X, Y, Z), oshape, *geo)
     if check:
         st = sparse_plan_status(plan)
@@ -377,8 +398,9 @@ def build_sparse_map(coords: torch.Tensor, shape, ks: int, stride: int, pad: int
 
 def sparse_plan_status(plan: SparsePlan) -> int:
     out = ctypes.c_int32(-1)
-    _check("ssc_sparse_plan_status", lib().ssc_sparse_plan_status(_ptr(plan.buf), plan.n_out, _stream(plan.device),
-                                                                  ctypes.byref(out)))
+    with _on(plan.device):
+        _check("ssc_sparse_plan_status", lib().ssc_sparse_plan_status(_ptr(plan.buf), plan.n_out, _stream(plan.device),
+                                                                      ctypes.byref(out)))
     return int(out.value)
 
 
@@ -405,10 +427,11 @@ def sparse_conv3d_fwd(plan: SparsePlan, feats: torch.Tensor, weight: torch.Tenso
     _need(out, "out", dt, (plan.n_out, co), dev)
     if ws is None:
         ws = sparse_workspace(plan, ci, co, dt)
-    _check("ssc_sparse_conv3d_fwd",
-           lib().ssc_sparse_conv3d_fwd(_ptr(plan.buf), plan.n_in, plan.n_out, plan.ks, _ptr(plan.perm), ci, co,
-                                       DTYPE_CODE[dt], _ptr(feats), _ptr(weight), _ptr(bias), _ptr(out), _ptr(ws),
-                                       ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_sparse_conv3d_fwd",
+               lib().ssc_sparse_conv3d_fwd(_ptr(plan.buf), plan.n_in, plan.n_out, plan.ks, _ptr(plan.perm), ci, co,
+                                           DTYPE_CODE[dt], _ptr(feats), _ptr(weight), _ptr(bias), _ptr(out), _ptr(ws),
+                                           ws.numel(), _stream(dev)))
     return out
 
 
@@ -430,10 +453,11 @@ def sparse_conv3d_bwd(plan: SparsePlan, feats: torch.Tensor, weight: torch.Tenso
         db = torch.empty((co,), dtype=dt, device=dev) if need_dbias else None
     if ws is None:
         ws = sparse_workspace(plan, ci, co, dt)
-    _check("ssc_sparse_conv3d_bwd",
-           lib().ssc_sparse_conv3d_bwd(_ptr(plan.buf), plan.n_in, plan.n_out, plan.ks, _ptr(plan.perm), ci, co,
-                                       DTYPE_CODE[dt], _ptr(feats), _ptr(weight), _ptr(dout), _ptr(dX), _ptr(dW),
-                                       _ptr(db), _ptr(ws), ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_sparse_conv3d_bwd",
+               lib().ssc_sparse_conv3d_bwd(_ptr(plan.buf), plan.n_in, plan.n_out, plan.ks, _ptr(plan.perm), ci, co,
+                                           DTYPE_CODE[dt], _ptr(feats), _ptr(weight), _ptr(dout), _ptr(dX), _ptr(dW),
+                                           _ptr(db), _ptr(ws), ws.numel(), _stream(dev)))
     return dX, dW, db
 
 
@@ -499,8 +523,9 @@ def encode_seq(coords: torch.Tensor, shape, mode: str = "z_order") -> torch.Tens
     grid = _grid(shape)
     width = seq_code_width(grid)
     codes = torch.empty((n,), dtype=torch.int32 if width == 32 else torch.int64, device=dev)
-    _check("ssc_encode_seq", lib().ssc_encode_seq(_ptr(coords), n, *grid, _mode(mode), _ptr(codes), width,
-                                                  _stream(dev)))
+    with _on(dev):
+        _check("ssc_encode_seq", lib().ssc_encode_seq(_ptr(coords), n, *grid, _mode(mode), _ptr(codes), width,
+                                                      _stream(dev)))
     return codes
 
 
@@ -514,8 +539,9 @@ def decode_seq(codes: torch.Tensor, shape, mode: str = "z_order") -> torch.Tenso
     grid = _grid(shape)
     width = 32 if codes.dtype == torch.int32 else 64
     coords = torch.empty((n, 4), dtype=torch.int32, device=dev)
-    _check("ssc_decode_seq", lib().ssc_decode_seq(_ptr(codes), n, *grid, _mode(mode), width, _ptr(coords),
-                                                  _stream(dev)))
+    with _on(dev):
+        _check("ssc_decode_seq", lib().ssc_decode_seq(_ptr(codes), n, *grid, _mode(mode), width, _ptr(coords),
+                                                      _stream(dev)))
     return coords
 
 
@@ -541,9 +567,10 @@ def grid_sample_fwd(plan: Plan, feats: torch.Tensor, points: torch.Tensor,
         out = torch.empty((m, c), dtype=dt, device=dev)
     _need(out, "out", dt, (m, c), dev)
     B, X, Y, Z = plan.shape
-    _check("ssc_grid_sample_fwd",
-           lib().ssc_grid_sample_fwd(_ptr(plan.buf), n, B, X, Y, Z, plan.key_bits, c, DTYPE_CODE[dt], _ptr(feats),
-                                     _ptr(points), m, _ptr(out), _stream(dev)))
+    with _on(dev):
+        _check("ssc_grid_sample_fwd",
+               lib().ssc_grid_sample_fwd(_ptr(plan.buf), n, B, X, Y, Z, plan.key_bits, c, DTYPE_CODE[dt], _ptr(feats),
+                                         _ptr(points), m, _ptr(out), _stream(dev)))
     return out
 
 
@@ -565,9 +592,10 @@ def grid_sample_bwd(plan: Plan, points: torch.Tensor, dout: torch.Tensor, dfeats
             raise SSCError("ssc_grid_sample_workspace_bytes", 2)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     B, X, Y, Z = plan.shape
-    _check("ssc_grid_sample_bwd",
-           lib().ssc_grid_sample_bwd(_ptr(plan.buf), n, B, X, Y, Z, plan.key_bits, c, DTYPE_CODE[dt], _ptr(points),
-                                     m, _ptr(dout), _ptr(dfeats), _ptr(ws), ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("ssc_grid_sample_bwd",
+               lib().ssc_grid_sample_bwd(_ptr(plan.buf), n, B, X, Y, Z, plan.key_bits, c, DTYPE_CODE[dt], _ptr(points),
+                                         m, _ptr(dout), _ptr(dfeats), _ptr(ws), ws.numel(), _stream(dev)))
     return dfeats
 
 
