@@ -494,7 +494,8 @@ int ssc_qk_norm_rope_bwd(const ssc_norm_rope_shape* shape, const void* q, const 
  *   dq = scale sum dS_j k_j,  dk_j = scale sum dS_j q,
  * sums over rows including all query heads of a shared key head.  A row with
  * no key (an empty sample, every key masked, or every score -inf) gives zeros,
- * lse = -inf and no gradient; a masked key's row is never used, whatever it
+ * lse = -inf and no gradient (only an infinite query among the last kind makes
+ * dk the formula's 0 * inf); a masked key's row is never used, whatever it
  * holds, and its gradient is zero.  Rows before the first or from the last
  * offset belong to no sample: as queries they have no key, as keys no query.
  * Offsets must not decrease; they are taken into [0, rows].
