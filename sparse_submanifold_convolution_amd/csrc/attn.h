@@ -146,6 +146,10 @@ struct Elt<__bf16> {
   __device__ static __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 };
 
+// Probabilities and dS are rounded to a 16-bit type for the second products, whose operands they are: results have about
+// 1.4 times the error of ones only rounded at the end.  Their remainders as a second operand would take that out with two
+// to three more products on the backward pass's eight.
+//
 // Exponent offset of the 16-bit probabilities.  fp16 is subnormal below 2^-14, which rows over thousands of keys
 // reach, so its probabilities are held times a power of two that keeps the largest (1) below fp16's 65504; sums
 // accumulated from them are scaled back exactly.  bf16 and fp32 have fp32's exponents.
@@ -361,7 +365,10 @@ __device__ __forceinline__ void split_range(int tiles, int s, int n, int* first,
 }
 
 // Waves per SIMD the registers are held to.  Two waves overlap their matrix and vector phases: with one (and
-// accumulators in the second register half) the passes ran at 0.5 to 0.7 of their speed.
+// accumulators in the second register half) the passes ran at 0.5 to 0.7 of their speed.  Some forms keep more than these
+// limits hold and put registers into scratch, by the compiler's report: dQ over few rows with heads of 33 to 64 (6 to 45
+// registers a lane, most with a mask) and masked over 96 (1 to 4), dQ with heads of 65 to 96 (16 to 19 with a mask, 4 in
+// fp16 without), and fp32 with heads over 96: the masked few-rows forward 36, dQ over few rows 41 to 90, dK and dV 57.
 struct Cfg {
   int fwd_occ, dq_occ, dkv_occ;
 };
@@ -369,7 +376,7 @@ constexpr Cfg tile_cfg(int esize, int dp) {
   return dp <= 64 ? Cfg{2, 2, 2} : esize == 4 ? Cfg{1, 1, 1} : Cfg{2, dp == 96 ? 2 : 1, 2};
 }
 // Waves of a forward workgroup: eight for 16-bit heads of over 96, whose tiles (64 KiB) then serve both waves of every
-// SIMD (2 x 11.2k rows, 8 heads of 128: 1.11 -> 1.05 ms); narrower heads run alike with four.
+// SIMD (2 x 11.2k rows, 8 heads of 128, bf16: 1.08 -> 1.01 ms); narrower heads run alike with four.
 constexpr int fwd_waves(int esize, int dp) { return esize == 2 && dp == 128 ? 8 : 4; }
 
 // keeps a wave's LDS writes before the reads that follow; the hardware serves them in order
@@ -862,7 +869,7 @@ __device__ __forceinline__ float less_delta(float dp, float ndel, float mul) {
 //
 // Forms, tiles and bounds as the forward pass: 2 x 11.2k rows, 16 heads of 64, bf16, 2.0 ms (four products at
 // 1.0 PFLOP/s, MFMA busy 48 % of the cycles).  Heads of 72 to 96 stream 32-row tiles, whose smaller stage leaves
-// registers for a second wave per SIMD (8 heads of 96: 1.8 -> 1.5 ms).
+// registers for a second wave per SIMD (8 heads of 96: 2.0 -> 1.6 ms).
 template <typename T, int DP, int NW, bool MASK, bool FEW>
 __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
   constexpr int R = sizeof(T) == 4 || (!FEW && DP == 96) ? 32 : 64;

@@ -10,9 +10,11 @@
 // A group of L lanes (a power of two) owns one row's head, 16 bytes a lane, and walks several heads of its row, so a
 // row's cosines and sines are computed once per group.  Turns are multiplied and reduced to [-1/2, 1/2] in 64 bits:
 // the phase of a position near 2^31 is as exact as that of position 1.  Sums, the norm and the rotation are fp32 and
-// the result is rounded once.  The calls are bound by memory: each element is read once and written once (backward:
-// read twice, written once).  629k rows of 16 + 16 heads of 64, bf16: forward 0.95 ms (5.4 TB/s), backward 1.50 ms
-// (5.2 TB/s); a 1 GiB copy reaches 5.2 TB/s.
+// the result is rounded once.  Each element is read once and written once (backward: read twice, written once).  629k rows
+// of 16 + 16 heads of 64, bf16, interleaved: forward 0.95 ms (5.4 TB/s), backward 1.50 ms (5.2 TB/s), bound by memory: a
+// 1 GiB copy reaches 5.2 TB/s.  The halves layout's lanes form every angle of their elements and exchange partners, in
+// registers for two waves per SIMD: 2.9 and 4.3 TB/s in 16 bits (fp32, half as many elements a lane: 5.3 and 5.0); heads
+// that do not fill a power of two of vectors leave lanes idle (80, bf16, interleaved: 4.2 and 3.6 TB/s).
 
 #include <hip/hip_runtime.h>
 
