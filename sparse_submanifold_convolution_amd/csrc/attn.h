@@ -753,7 +753,11 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(Params p) {
 // values of others.  The maxima are formed by pieces: the rows of segment s within block g (`rows` of them) of one side
 // are piece g + s, which numbers the pieces in row order with no table of where a segment's begin, and each piece is one
 // workgroup's per key head.  Numbers that no row has (empty segments leave them) are never written nor read.
-constexpr int kPieceBlocks = 512;  // blocks of a side times key heads, at most: what the rows are spread over
+// Blocks of a side times key heads, at most.  Fewer leave the launch short of loads on their way (backward pass of 2 x 300k
+// keys of 4 heads, 8 rows each: 992 us with 128, 810 with 256, 715 with 512, 687 with 1,024), more are more to read for
+// every workgroup of a single key head (100k rows of 16 heads over 77 keys: 743 us with 512, 775 with 1,024, 851 with
+// 2,048; with four loads on their way together 686 with 512).
+constexpr int kPieceBlocks = 512;
 inline int piece_rows(int64_t rows, int64_t heads_kv, int64_t rows_least) {
   const int64_t blocks = kPieceBlocks / heads_kv > 0 ? kPieceBlocks / heads_kv : 1, n = (rows + blocks - 1) / blocks;
   return int(n > rows_least ? n : rows_least);
@@ -826,7 +830,17 @@ static_assert(SSC_MAX_HEAD_DIM <= 16 * 8, "a row is one vector a lane");
 __device__ __forceinline__ float top_of(const float* top, int rows, int64_t begin, int len, int index) {
   const int last = int((begin + len - 1) / rows) + index;
   float m = 0.f;
-  for (int i = int(begin / rows) + index + int(threadIdx.x & 63); i <= last; i += 64) m = fmaxf(m, top[i]);
+  // four loads on their way together; past the last piece they repeat it
+  for (int i = int(begin / rows) + index; i <= last; i += 256) {
+    float x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = i + 64 * u + int(threadIdx.x & 63);
+      x[u] = top[at < last ? at : last];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = fmaxf(m, x[u]);
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
   return m;
