@@ -550,6 +550,163 @@ int ssc_cross_attn_bwd(const ssc_attn_shape* shape, const void* q, const void* k
                        const int32_t* kv_offsets, const uint8_t* kv_mask, void* dq, void* dk, void* dv,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Windowed attention: cross attention in which a row sees only keys near its
+ * own place and the first few.  Row i of a sample (of `rows` rows and `keys`
+ * keys) sits at place t = i + keys - rows of the sample's keys, so that with
+ * as many rows as keys it sits at its own key and with fewer (new rows of a
+ * longer sequence) at the end; it sees the keys j (numbered within the sample)
+ *   j <= t + right  and  (j >= t - left  or  j < sinks)
+ * whose kv_mask byte is not zero: right = 0 is causal, and the first `sinks`
+ * keys stay visible to all later rows.  Formulas, sizes, strides, masks, rows
+ * of no sample and rounding are those of ssc_cross_attn_*; keys that no row of
+ * a sample sees are never used, whatever they hold, but an infinite or NaN key
+ * or value row that some row sees may also spoil rows up to a tile (of 256
+ * rows at most) away.  The time of a call follows the keys its rows see.
+ * ------------------------------------------------------------------------ */
+typedef struct ssc_attn_window {
+  int32_t left, right;                   /* keys before and behind a row's own place, at most SSC_MAX_ATTN_ROWS; -1: all */
+  int32_t sinks;                         /* first keys that stay visible, 0 .. SSC_MAX_ATTN_ROWS */
+} ssc_attn_window;
+
+/* Workspace bytes of ssc_window_attn_fwd (backward 0) or _bwd (backward 1); 0
+ * for invalid or unsupported arguments.  Needs no GPU. */
+size_t ssc_window_attn_workspace_bytes(const ssc_attn_shape* shape, const ssc_attn_window* window, int32_t backward);
+
+/* Arguments as ssc_cross_attn_fwd's and _bwd's. */
+int ssc_window_attn_fwd(const ssc_attn_shape* shape, const ssc_attn_window* window, const void* q, const void* k,
+                        const void* v, const int32_t* q_offsets, const int32_t* kv_offsets, const uint8_t* kv_mask,
+                        void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+int ssc_window_attn_bwd(const ssc_attn_shape* shape, const ssc_attn_window* window, const void* q, const void* k,
+                        const void* v, const void* out, const float* lse, const void* dout, const int32_t* q_offsets,
+                        const int32_t* kv_offsets, const uint8_t* kv_mask, void* dq, void* dk, void* dv,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm of feature rows, with the sum of a residual stream and dropout in
+ * the same pass.  Per row of `channels` elements:
+ *   s = x,  or with a residual  s = residual + dropout(x),
+ *   mean = sum s / channels,  r = 1 / sqrt(sum (s - mean)^2 / channels + eps),
+ *   y = (s - mean) r weight + bias;
+ * backward, with z = (s - mean) r and g = dy weight:
+ *   dresidual = r (g - mean(g) - z mean(g z)) + ds,  dx = dropout(dresidual),
+ *   dweight = sum over rows of dy z,  dbias = sum over rows of dy.
+ * Sums and statistics are fp32, results are rounded once (y is formed from s
+ * before its rounding), weight gradients are summed in a fixed order.
+ *
+ * Dropout keeps element e of a tensor (its row-major number) where sixteen
+ * random bits are at least t = round(65536 p), and multiplies what it keeps by
+ * 65536 / (65536 - t); a dropped element is zero whatever x holds there.  The
+ * bits are half-word e mod 8 (a word's low half first) of Philox-4x32 with ten
+ * rounds at counter (e / 8, layer, step low, step high) under key (seed low,
+ * seed high), so nothing is stored: the backward pass makes the same choice
+ * from the same rng and layer.  rng is {seed, step} in device memory, read by
+ * the kernels, so a captured call follows its changes.
+ * ------------------------------------------------------------------------ */
+#define SSC_MAX_SEQ_ROWS (1LL << 28)
+#define SSC_MAX_SEQ_CHANNELS 8192
+
+/* Sizes of a call (a host struct, read during the call). */
+typedef struct ssc_layer_norm_shape {
+  int64_t n;                             /* rows, at most SSC_MAX_SEQ_ROWS; a row takes a lane per 16 bytes (4, 8, .. 64
+                                          * or 256), fewer than 2^32 in all */
+  int64_t x_row_stride;                  /* elements, multiples of 16 bytes, not negative: of x (backward: of s) */
+  int64_t residual_row_stride;
+  double p;                              /* chance to drop, in [0, 1); needs a residual and at most 2^35 elements */
+  int32_t channels;                      /* whole 16-byte vectors, at most SSC_MAX_SEQ_CHANNELS */
+  int32_t dtype;
+  int32_t layer;                         /* of the network's dropouts, not negative */
+  float eps;
+} ssc_layer_norm_shape;
+
+/*
+ * x and residual (or NULL) [n][channels] (strided), weight and bias [channels]
+ * or NULL (ones, zeros), rng {seed, step} (8-byte aligned; may be NULL where
+ * p rounds to no dropout).  y [n][channels] and, with a residual, s
+ * [n][channels], both contiguous, out; they may not overlap the inputs.
+ */
+int ssc_layer_norm_fwd(const ssc_layer_norm_shape* shape, const void* x, const void* residual, const void* weight,
+                       const void* bias, const int64_t* rng, void* y, void* s, void* stream);
+
+/* Workspace bytes of ssc_layer_norm_bwd; 0 for invalid or unsupported
+ * arguments.  Needs no GPU. */
+size_t ssc_layer_norm_workspace_bytes(const ssc_layer_norm_shape* shape);
+
+/*
+ * Backward pass: s as the forward pass wrote it (x itself without a
+ * residual), dy and ds (the output gradient of s, or NULL) contiguous; dx,
+ * dresidual contiguous, dweight, dbias, out, each NULL to skip it.  Without
+ * dropout dx and dresidual are equal.  The workspace is used only when a
+ * weight's or bias's gradient is asked for.
+ */
+int ssc_layer_norm_bwd(const ssc_layer_norm_shape* shape, const void* s, const void* dy, const void* ds,
+                       const void* weight, const int64_t* rng, void* dx, void* dresidual, void* dweight, void* dbias,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * y = dropout(x), or residual + dropout(x), of `elements` contiguous elements
+ * (at most 2^35; rng, layer and p as above).  The gradient of x is the same
+ * call on the output gradient without a residual; the residual's is the output
+ * gradient itself.
+ */
+int ssc_dropout(int64_t elements, int32_t dtype, double p, int32_t layer, const void* x, const void* residual,
+                const int64_t* rng, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence along the rows of ragged samples: rows offsets[b] ..
+ * offsets[b + 1] - 1 of sample b, from the first (reverse: from the last).
+ * Per channel, with a = sigmoid(gate):
+ *   h_t = a_t h_{t-1} + (1 - a_t) x_t   (SSC_SCAN_MIX)
+ *   h_t = a_t h_{t-1} + x_t             (SSC_SCAN_SUM),
+ * h0[b] (zeros without one) before the first row; y is every row's h, last[b]
+ * the final state, h0[b] for a sample with no rows.  Backward, with the output
+ * gradients dy and dlast (or none):
+ *   D_t = dy_t + a_{t+1} D_{t+1}  (the final row: + dlast[b]),
+ *   dx_t = (1 - a_t) D_t  or  D_t,
+ *   dgate_t = a_t (1 - a_t) D_t (h_{t-1} - x_t  or  h_{t-1}),  dh0[b] = a_1 D_1.
+ * Rows of no sample give zeros and take no part.  Offsets must not decrease;
+ * they are taken into [0, n].  States, sums and products are fp32, and states
+ * stay fp32 between calls.  Samples do not depend on each other's values;
+ * results repeat.
+ * ------------------------------------------------------------------------ */
+enum ssc_scan_form { SSC_SCAN_MIX = 0, SSC_SCAN_SUM = 1 };
+
+/* Sizes of a call (a host struct, read during the call). */
+typedef struct ssc_scan_shape {
+  int64_t n;                             /* rows, at most SSC_MAX_SEQ_ROWS; a workgroup of 256 threads takes 128 rows of
+                                          * 256 bytes (256 of 128, 512 of 64 where the rows are no longer), with fewer
+                                          * than 2^32 threads in all */
+  int64_t x_row_stride, gate_row_stride; /* elements, multiples of 16 bytes, not negative */
+  int32_t batch;                         /* samples, 1 .. SSC_MAX_ATTN_BATCH */
+  int32_t channels;                      /* whole 16-byte vectors, at most SSC_MAX_SEQ_CHANNELS */
+  int32_t dtype;
+  int32_t form;                          /* ssc_scan_form */
+  int32_t reverse;
+} ssc_scan_shape;
+
+/* Bytes of the states that the backward pass takes over from the forward
+ * pass, and workspace bytes of either pass; 0 for invalid or unsupported
+ * arguments.  Need no GPU. */
+size_t ssc_gated_scan_carry_bytes(const ssc_scan_shape* shape);
+size_t ssc_gated_scan_workspace_bytes(const ssc_scan_shape* shape);
+
+/*
+ * x and gate [n][channels] (strided), offsets [batch + 1] int32 in device
+ * memory, h0 [batch][channels] fp32 or NULL.  y [n][channels] contiguous,
+ * last [batch][channels] fp32, out; carries (out) for the backward pass, or
+ * NULL.
+ */
+int ssc_gated_scan_fwd(const ssc_scan_shape* shape, const void* x, const void* gate, const int32_t* offsets,
+                       const float* h0, void* y, float* last, float* carries, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Backward pass: carries as the forward pass wrote them, dy contiguous, dlast
+ * [batch][channels] fp32 or NULL; dx, dgate contiguous, out; dh0
+ * [batch][channels] fp32, out, or NULL to skip it. */
+int ssc_gated_scan_bwd(const ssc_scan_shape* shape, const void* x, const void* gate, const float* carries,
+                       const void* dy, const int32_t* offsets, const float* h0, const float* dlast, void* dx,
+                       void* dgate, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code (host only). */
 const char* ssc_status_string(int status);
 

@@ -24,6 +24,7 @@ STATUS_NAMES = {0: "SSC_OK", 1: "SSC_ERR_INVALID_ARG", 2: "SSC_ERR_UNSUPPORTED",
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 _VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_F64 = ctypes.c_double
 SIGNATURES = {
     "ssc_plan_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32, _I32]),
     "ssc_build_neighbor_map": (ctypes.c_int, [_VP, _I64, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _SZ, _VP]),
@@ -65,6 +66,17 @@ SIGNATURES = {
     "ssc_cross_attn_workspace_bytes": (_SZ, [_VP, _I32]),
     "ssc_cross_attn_fwd": (ctypes.c_int, [_VP] * 10 + [_SZ, _VP]),
     "ssc_cross_attn_bwd": (ctypes.c_int, [_VP] * 14 + [_SZ, _VP]),
+    "ssc_window_attn_workspace_bytes": (_SZ, [_VP, _VP, _I32]),
+    "ssc_window_attn_fwd": (ctypes.c_int, [_VP] * 11 + [_SZ, _VP]),
+    "ssc_window_attn_bwd": (ctypes.c_int, [_VP] * 15 + [_SZ, _VP]),
+    "ssc_layer_norm_fwd": (ctypes.c_int, [_VP] * 9),
+    "ssc_layer_norm_workspace_bytes": (_SZ, [_VP]),
+    "ssc_layer_norm_bwd": (ctypes.c_int, [_VP] * 11 + [_SZ, _VP]),
+    "ssc_gated_scan_carry_bytes": (_SZ, [_VP]),
+    "ssc_gated_scan_workspace_bytes": (_SZ, [_VP]),
+    "ssc_gated_scan_fwd": (ctypes.c_int, [_VP] * 9 + [_SZ, _VP]),
+    "ssc_gated_scan_bwd": (ctypes.c_int, [_VP] * 12 + [_SZ, _VP]),
+    "ssc_dropout": (ctypes.c_int, [_I64, _I32, _F64, _I32, _VP, _VP, _VP, _VP, _VP]),
 }
 
 SEQ_MODES = {"z_order": 0, "hilbert": 1}

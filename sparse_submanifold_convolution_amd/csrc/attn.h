@@ -15,6 +15,12 @@
 // Query heads sharing a key head are packed along the rows: row r of a sample and key head hk is token r / G,
 // head hk * G + r mod G (G = heads_q / heads_kv).  dK and dV of a shared head thereby sum over its query heads in a
 // fixed order, and one query token's G heads share a tile.
+//
+// WIN: windowed attention.  Token i of a sample sits at place t = i + (keys - tokens) of the sample's keys and sees the
+// keys j <= t + right with j >= t - left or j < sinks.  A workgroup streams only the rows that one of its columns sees:
+// the sinks' tiles, then tiles that begin with the first row of its columns' windows and end with the last one's, so
+// rows that no column sees are not read.  Tiles that every column of a wave sees whole skip the comparison; the others
+// turn a column's bounds into a word of a bit per streamed row.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,6 +61,7 @@ struct Params {
   int32_t gshift;      // r / G = (r * gmul) >> gshift for r < 2^31
   float scale;
   int32_t tiles, nsplit;
+  int32_t left, right, sinks;  // WIN
   // splits: partial sums [nsplit][rows][d]; forward part_b: [nsplit][rows][2] (max, sum); dQ part_e: [nsplit][rows][2]
   float *part_a, *part_b, *part_e;
 };
@@ -307,10 +314,10 @@ struct Segment {
   int32_t index;   // of the segment: 0 before the first sample, b + 1 for sample b
 };
 
-// Finds tile t of the concatenated segments, each holding ceil(len * mult / cols) tiles; false past the last.  Each
-// lane looks at one segment; all offsets are loaded side by side.
+// Finds tile t of the concatenated segments, each holding ceil(len * mult / cols) tiles (most: of its first rows, and of
+// the samples' only); false past the last.  Each lane looks at one segment; all offsets are loaded side by side.
 __device__ __forceinline__ bool find_segment(const int32_t* off, int64_t n, const int32_t* other_off, int64_t other_n,
-                                             int batch, int mult, int cols, int t, Segment* seg) {
+                                             int batch, int mult, int cols, int t, Segment* seg, int most = 0x7FFFFFFF) {
   const int lane = threadIdx.x & 63;
   for (int base = 0; base < batch + 2; base += 64) {
     const int s = base + lane;
@@ -321,7 +328,8 @@ __device__ __forceinline__ bool find_segment(const int32_t* off, int64_t n, cons
     if (s == batch + 1) e = n;
     if (e < b || s > batch + 1) e = b;
     const int len = int(e - b), olen = s >= 1 && s <= batch && oe > ob ? int(oe - ob) : 0;
-    const int mine = int((int64_t(len) * mult + cols - 1) / cols);
+    const int head = most == 0x7FFFFFFF ? len : (s < 1 || s > batch ? 0 : (len < most ? len : most));
+    const int mine = int((int64_t(head) * mult + cols - 1) / cols);
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -362,6 +370,33 @@ __device__ __forceinline__ void split_range(int tiles, int s, int n, int* first,
   const int per = (tiles + n - 1) / n;
   *first = s * per < tiles ? s * per : tiles;
   *last = *first + per < tiles ? *first + per : tiles;
+}
+
+// bits 0 .. n - 1
+__device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1); }
+
+// The key rows that a workgroup's query columns see (WIN): the sinks' tiles, then the window's, each R rows.  Where the
+// two meet they are one run of tiles from row 0.
+struct Seen {
+  int sink_tiles, sink_end, first, end, tiles;
+  // place0, place1: of the first and the last column
+  __device__ __forceinline__ void init(const Params& p, int place0, int place1, int keys, int R) {
+    end = place1 + p.right + 1;
+    end = end < 0 ? 0 : (end < keys ? end : keys);
+    first = place0 - p.left;
+    first = first < 0 ? 0 : (first < end ? first : end);
+    sink_end = p.sinks < end ? p.sinks : end;
+    if (first <= sink_end) first = sink_end = 0;
+    sink_tiles = (sink_end + R - 1) / R;
+    tiles = sink_tiles + (end - first + R - 1) / R;
+  }
+  __device__ __forceinline__ int row(int t, int R) const { return t < sink_tiles ? t * R : first + (t - sink_tiles) * R; }
+  __device__ __forceinline__ int rows(int t, int R) const { return (t < sink_tiles ? sink_end : end) - row(t, R); }
+};
+
+// bit k: whether the column at `place` sees key row0 + k
+__device__ __forceinline__ uint64_t sees(const Params& p, int place, int row0) {
+  return below(place + p.right + 1 - row0) & (~below(place - p.left - row0) | below(p.sinks - row0));
 }
 
 // Waves per SIMD the registers are held to.  Two waves overlap their matrix and vector phases: with one (and
@@ -448,7 +483,7 @@ __device__ __forceinline__ float lse_of(const Params& p, float m, float total) {
 // with one barrier a tile.  FEW (a sample's rows fit 32 columns: single tokens while serving): the waves share the
 // columns and take the tiles in turn, each through an LDS tile of its own with no barrier, and join their sums at the
 // end; four rows pooling 0.8M keys, 4 heads of 64, run at 5.2 TB/s.
-template <typename T, int DP, int NW, bool MASK, bool FEW>
+template <typename T, int DP, int NW, bool MASK, bool FEW, bool WIN>
 __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd_occ) fwd_kernel(Params p) {
   using TL = TileOf<T, DP>;
   using E = Elt<T>;
@@ -488,28 +523,47 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
   for (int d = 0; d < TL::kBlocks; ++d) o[d] = f32x16{};
 
   int t0, t1;
-  split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
+  Seen seen;
+  int place = 0, place0 = 0, place1 = 0;  // of this lane's column, of the wave's first and last ones
+  if constexpr (WIN) {
+    const int shift = sg.other_len - sg.len, lastr = int(uint32_t(sg.len) * uint32_t(p.G)) - 1;
+    auto at = [&](int c) { return int(div_g(uint32_t(c < lastr ? c : lastr), p)) + shift; };
+    const int c0 = sg.tile * TC, w0 = c0 + (FEW ? 0 : wave * 32);
+    place = at(w0 + (lane & 31));
+    place0 = at(w0);
+    place1 = at(w0 + 31);
+    seen.init(p, at(c0), at(c0 + TC - 1), sg.other_len, TL::kRows);
+  }
+  split_range(WIN ? seen.tiles : (sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
   constexpr int step = FEW ? NW : 1;
   if (FEW) t0 += wave;
   const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
   Walk<TL::kRows> wk, wv;
   wk.init(p.k_row * int64_t(sizeof(T)), head_bytes);
   wv.init(p.v_row * int64_t(sizeof(T)), head_bytes);
-  wk.at = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head) + t0 * wk.step;
-  wv.at = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head) + t0 * wv.step;
+  const char* k0 = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head);
+  const char* v0 = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head);
+  wk.at = k0 + t0 * wk.step;
+  wv.at = v0 + t0 * wv.step;
   Stage<T, DP, NT> sk, sv;
   sk.init(wk.row_bytes, dchunks);
   sv.init(wv.row_bytes, dchunks);
   uint8_t keep[Stage<T, DP, NT>::N];
   bool kept = false;  // the key of streamed row `lane`
   auto load = [&](int t) {
-    const int rows = sg.other_len - t * TL::kRows;
+    const int rows = WIN ? seen.rows(t, TL::kRows) : sg.other_len - t * TL::kRows;
+    if constexpr (WIN) {
+      wk.at = k0 + int64_t(seen.row(t, TL::kRows)) * wk.row_bytes;
+      wv.at = v0 + int64_t(seen.row(t, TL::kRows)) * wv.row_bytes;
+    }
     sk.load(wk.at, wk.span(rows));
     sv.load(wv.at, wv.span(rows));
-    wk.at += step * wk.step;
-    wv.at += step * wv.step;
+    if constexpr (!WIN) {
+      wk.at += step * wk.step;
+      wv.at += step * wv.step;
+    }
     if constexpr (MASK) {
-      const uint8_t* mp = p.mask + sg.other + int64_t(t) * TL::kRows;
+      const uint8_t* mp = p.mask + sg.other + (WIN ? int64_t(seen.row(t, TL::kRows)) : int64_t(t) * TL::kRows);
 #pragma unroll
       for (int i = 0; i < Stage<T, DP, NT>::N; ++i) {
         const int r = Stage<T, DP, NT>::item(i) / TL::CPR;
@@ -537,13 +591,22 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
       wave_fence();  // LDS serves a wave's accesses in order
     else
       __syncthreads();
-    const int rows = sg.other_len - t * TL::kRows;
+    const int rows = WIN ? seen.rows(t, TL::kRows) : sg.other_len - t * TL::kRows;
     if constexpr (!MASK)
       valid = rows >= TL::kRows ? kAll : (1ull << rows) - 1;
     else if constexpr (!FEW)
       valid = lvalid[buf];
     if (t + step < t1) load(t + step);
     if (MASK && valid == 0) continue;
+    bool part = valid != kAll;  // some row is not seen by some column
+    if constexpr (WIN) {
+      const int row0 = seen.row(t, TL::kRows);
+      if (row0 < place1 - p.left || row0 + TL::kRows - 1 > place0 + p.right) {
+        valid &= sees(p, place, row0);
+        if (!__any(valid != 0)) continue;
+        part = true;
+      }
+    }
 
     f32x16 s[TL::kGroups];
 #pragma unroll
@@ -556,7 +619,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).fwd
         s[kb] = E::mma(a, qf[f], s[kb]);
       }
     }
-    if (valid != kAll) {
+    if (part) {
 #pragma unroll
       for (int kb = 0; kb < TL::kGroups; ++kb) {
         const uint32_t w = uint32_t(valid >> (32 * kb)) >> (4 * half);
@@ -884,7 +947,7 @@ __device__ __forceinline__ float less_delta(float dp, float ndel, float mul) {
 // Forms, tiles and bounds as the forward pass: 2 x 11.2k rows, 16 heads of 64, bf16, 2.0 ms (four products at
 // 1.0 PFLOP/s, MFMA busy 48 % of the cycles).  Heads of 72 to 96 stream 32-row tiles, whose smaller stage leaves
 // registers for a second wave per SIMD (8 heads of 96: 2.0 -> 1.6 ms).
-template <typename T, int DP, int NW, bool MASK, bool FEW>
+template <typename T, int DP, int NW, bool MASK, bool FEW, bool WIN>
 __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_occ) dq_kernel(Params p) {
   constexpr int R = sizeof(T) == 4 || (!FEW && DP == 96) ? 32 : 64;
   using TL = TileOf<T, DP, R>;
@@ -932,28 +995,47 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_
   }
 
   int t0, t1;
-  split_range((sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
+  Seen seen;
+  int place = 0, place0 = 0, place1 = 0;  // of this lane's column, of the wave's first and last ones
+  if constexpr (WIN) {
+    const int shift = sg.other_len - sg.len, lastr = int(uint32_t(sg.len) * uint32_t(p.G)) - 1;
+    auto at = [&](int c) { return int(div_g(uint32_t(c < lastr ? c : lastr), p)) + shift; };
+    const int c0 = sg.tile * TC, w0 = c0 + (FEW ? 0 : wave * 32);
+    place = at(w0 + (lane & 31));
+    place0 = at(w0);
+    place1 = at(w0 + 31);
+    seen.init(p, at(c0), at(c0 + TC - 1), sg.other_len, TL::kRows);
+  }
+  split_range(WIN ? seen.tiles : (sg.other_len + TL::kRows - 1) / TL::kRows, split, p.nsplit, &t0, &t1);
   constexpr int step = FEW ? NW : 1;
   if (FEW) t0 += wave;
   const uint32_t head_bytes = uint32_t(p.d) * uint32_t(sizeof(T));
   Walk<TL::kRows> wk, wv;
   wk.init(p.k_row * int64_t(sizeof(T)), head_bytes);
   wv.init(p.v_row * int64_t(sizeof(T)), head_bytes);
-  wk.at = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head) + t0 * wk.step;
-  wv.at = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head) + t0 * wv.step;
+  const char* k0 = reinterpret_cast<const char*>(static_cast<const T*>(p.k) + sg.other * p.k_row + hk * p.k_head);
+  const char* v0 = reinterpret_cast<const char*>(static_cast<const T*>(p.v) + sg.other * p.v_row + hk * p.v_head);
+  wk.at = k0 + t0 * wk.step;
+  wv.at = v0 + t0 * wv.step;
   Stage<T, DP, NT, R> sk, sv;
   sk.init(wk.row_bytes, dchunks);
   sv.init(wv.row_bytes, dchunks);
   uint8_t keep[Stage<T, DP, NT, R>::N];
   bool kept = false;
   auto load = [&](int t) {
-    const int rows = sg.other_len - t * TL::kRows;
+    const int rows = WIN ? seen.rows(t, TL::kRows) : sg.other_len - t * TL::kRows;
+    if constexpr (WIN) {
+      wk.at = k0 + int64_t(seen.row(t, TL::kRows)) * wk.row_bytes;
+      wv.at = v0 + int64_t(seen.row(t, TL::kRows)) * wv.row_bytes;
+    }
     sk.load(wk.at, wk.span(rows));
     sv.load(wv.at, wv.span(rows));
-    wk.at += step * wk.step;
-    wv.at += step * wv.step;
+    if constexpr (!WIN) {
+      wk.at += step * wk.step;
+      wv.at += step * wv.step;
+    }
     if constexpr (MASK) {
-      const uint8_t* mp = p.mask + sg.other + int64_t(t) * TL::kRows;
+      const uint8_t* mp = p.mask + sg.other + (WIN ? int64_t(seen.row(t, TL::kRows)) : int64_t(t) * TL::kRows);
 #pragma unroll
       for (int i = 0; i < Stage<T, DP, NT, R>::N; ++i) {
         const int r = Stage<T, DP, NT, R>::item(i) / TL::CPR;
@@ -981,16 +1063,22 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_
       wave_fence();
     else
       __syncthreads();
-    const int rows = sg.other_len - t * TL::kRows;
+    const int rows = WIN ? seen.rows(t, TL::kRows) : sg.other_len - t * TL::kRows;
     if constexpr (!MASK)
       valid = rows >= TL::kRows ? kAll : (1ull << rows) - 1;
     else if constexpr (!FEW)
       valid = lvalid[buf];
     if (t + step < t1) load(t + step);
+    bool bounds = false;  // WIN: the columns see different rows
+    if constexpr (WIN) {
+      const int row0 = seen.row(t, TL::kRows);
+      bounds = row0 < place1 - p.left || row0 + TL::kRows - 1 > place0 + p.right;
+      if (bounds) valid &= sees(p, place, row0);
+    }
 #pragma unroll
     for (int kb = 0; kb < TL::kGroups; ++kb) {
       const uint32_t vw = uint32_t(valid >> (32 * kb));
-      if (vw == 0) continue;
+      if (WIN ? !__any(vw != 0) : vw == 0) continue;
       f32x16 s{}, dp{};
 #pragma unroll
       for (int f = 0; f < TL::kFrags; ++f) {
@@ -1001,7 +1089,7 @@ __global__ void __launch_bounds__(NW * 64, FEW ? 2 : tile_cfg(sizeof(T), DP).dq_
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, sh));
-      if (~vw != 0) {
+      if (WIN ? bounds || __any(~vw != 0) : ~vw != 0) {
         const uint32_t w = vw >> (4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
@@ -1174,8 +1262,12 @@ __global__ void __launch_bounds__(256) dq_join_kernel(Params p) {
 // tile: 2 x 11.2k rows, 16 heads of 64, bf16, 2.0 ms (four products at 1.0 PFLOP/s, MFMA busy 49 % of the cycles).  A
 // software pipeline over 32-row blocks measured the same for heads of 64 and 10 to 60 % longer for 32 and for fp32.
 // DK, DV: the gradients a launch forms.
-template <typename T, int DP, int NW, bool MASK, bool DK, bool DV>
-__global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
+//
+// WIN: a key past the sinks is seen by the tokens of places j - right .. j + left, which its workgroup streams.  The
+// sinks are seen by all later tokens: they are columns of a launch of their own (SINK), of single waves, whose long
+// streams are split and whose sums are joined by sink_join_kernel.
+template <typename T, int DP, int NW, bool MASK, bool DK, bool DV, bool WIN, bool SINK>
+__global__ void __launch_bounds__(NW * 64, SINK ? 1 : tile_cfg(sizeof(T), DP).dkv_occ) dkv_kernel(Params p) {
   constexpr int R = sizeof(T) == 4 || DP > 64 ? 32 : 64;
   using TL = TileOf<T, DP, R>;
   using E = Elt<T>;
@@ -1186,7 +1278,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   if (item >= int64_t(p.tiles) * p.hk * p.nsplit) return;
   const int tile = int(item % p.tiles), hk = int(item / p.tiles % p.hk), split = int(item / p.tiles / p.hk);
   Segment sg;
-  if (!find_segment(p.koff, p.nk, p.qoff, p.nq, p.batch, 1, TC, tile, &sg)) return;
+  if (!find_segment(p.koff, p.nk, p.qoff, p.nq, p.batch, 1, TC, tile, &sg, SINK ? p.sinks : 0x7FFFFFFF)) return;
   const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
   const int dchunks = p.d / TL::kVec;
   const float c = p.scale * kLog2e;
@@ -1194,7 +1286,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);
 
   const int col = sg.tile * TC + wave * 32 + (lane & 31);
-  const bool live = col < sg.len;
+  const bool live = col < sg.len && (!WIN || (SINK ? col < p.sinks : col >= p.sinks || sg.index == 0 || sg.index > p.batch));
   const int64_t row = sg.begin + (live ? col : 0);
   const bool on = live && (!MASK || p.mask[row] != 0);
   u32x4 kf[TL::kFrags], vf[DK ? TL::kFrags : 1];
@@ -1210,7 +1302,24 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   };
   clear();
   // waves whose columns all lie past the sample's keys only help to stage
-  const bool busy = sg.tile * TC + wave * 32 < sg.len;
+  const bool busy = WIN ? __any(live) : sg.tile * TC + wave * 32 < sg.len;
+  // WIN: only the tokens that see one of the workgroup's columns; tokens [see0, see1) see this lane's
+  int see0 = 0, see1 = 0, full0 = 0, full1 = 0;
+  if constexpr (WIN) {
+    const int shift = sg.len - sg.other_len, tokens = sg.other_len;
+    const int j0 = SINK || sg.tile * TC > p.sinks ? sg.tile * TC : p.sinks;
+    const int j1 = (sg.tile + 1) * TC < sg.len ? (sg.tile + 1) * TC : sg.len;
+    int lo = j0 - p.right - shift, hi = SINK ? tokens : j1 - 1 + p.left - shift + 1;
+    lo = lo < 0 ? 0 : lo;
+    hi = hi < tokens ? hi : tokens;
+    const int w0 = sg.tile * TC + wave * 32;
+    see0 = col - p.right - shift - lo;
+    see1 = SINK ? 0x3FFFFFFF : col + p.left - shift + 1 - lo;
+    full0 = w0 + 31 - p.right - shift - lo;  // rows [full0, full1) of the stream are seen by all of the wave's columns
+    full1 = SINK ? 0x3FFFFFFF : w0 + p.left - shift + 1 - lo;
+    sg.other += lo;
+    sg.other_len = j0 < j1 && hi > lo ? hi - lo : 0;
+  }
 
   // the sample's queries, head after head of the group: tile n is head n / tiles, its tile n mod tiles
   const int tiles = (sg.other_len + R - 1) / R;
@@ -1264,6 +1373,7 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
     }
   };
   const int n = n1 - n0;
+  int done = WIN && n > 0 ? (n0 - g * tiles) * R : 0;  // first row of the tile at hand
   if (n > 0) {
     seek();
     load();
@@ -1273,9 +1383,20 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
     store(buf);
     __syncthreads();
     if (i + 1 < n) load();
-    if (!busy) continue;
+    if (!busy) continue;  // for the whole pass
     const char* tq = lds[buf];
     const char* td = tq + TL::kBytes;
+    uint64_t vis = ~0ull;
+    bool part = false;  // WIN: some column does not see some of the tile's rows
+    if constexpr (WIN) {
+      const int r0 = done;
+      done = done + R < sg.other_len ? done + R : 0;  // the next head's rows begin anew
+      part = r0 < full0 || r0 + R > full1;
+      if (part) {
+        vis = below(see1 - r0) & ~below(see0 - r0);
+        if (!__any(vis != 0)) continue;
+      }
+    }
     f32x16 s[G], dp[G];
 #pragma unroll
     for (int b = 0; b < G; ++b) {
@@ -1297,9 +1418,18 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
         const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float pr = __builtin_amdgcn_exp2f(fmaf(s[b][4 * i + j], c, sh[j]));
+          float pr = __builtin_amdgcn_exp2f(fmaf(s[b][4 * i + j], c, sh[j]));
+          float ds = 0.f;
+          if constexpr (DK) ds = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
+          if constexpr (WIN)
+            if (part) {
+              // both: what a key that is not seen holds does not matter
+              const bool on = (uint32_t(vis >> (32 * b)) >> (8 * i + 4 * half + j)) & 1u;
+              pr = on ? pr : 0.f;
+              ds = on ? ds : 0.f;
+            }
           s[b][4 * i + j] = pr;
-          if constexpr (DK) dp[b][4 * i + j] = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
+          if constexpr (DK) dp[b][4 * i + j] = ds;
         }
       }
 #pragma unroll
@@ -1319,7 +1449,10 @@ __global__ void __launch_bounds__(NW * 64, tile_cfg(sizeof(T), DP).dkv_occ) dkv_
   if (!live) return;
   // a masked key has no gradient, whatever its zeroed column collected
   if (!on) clear();
-  const int64_t o = (row * p.hk + hk) * p.d, sp = int64_t(split) * p.nk * p.hk * p.d + o;
+  const int64_t o = (row * p.hk + hk) * p.d;
+  // a sink's partial sums are numbered by its tile's columns
+  const int64_t sp = SINK ? (((int64_t(split) * p.tiles + tile) * TC + (lane & 31)) * p.hk + hk) * p.d
+                          : int64_t(split) * p.nk * p.hk * p.d + o;
   if constexpr (DK)
     store_cols<T, DP>(static_cast<T*>(p.dk) + o, p.nsplit > 1 ? p.part_a + sp : nullptr, dk, p.d, ldexpf(p.scale, -dse));
   if constexpr (DV)
@@ -1349,6 +1482,28 @@ __global__ void __launch_bounds__(64) sum_splits_kernel(const float* part_k, con
     reinterpret_cast<uint2*>(dst)[i] = make_uint2(Elt<T>::pack2(a.x, a.y), Elt<T>::pack2(a.z, a.w));
 }
 
+constexpr int kSinkCols = 32;  // keys of a sink launch's tile: one wave's columns
+
+// The sinks' dK (blockIdx.y 0) and dV (1): a workgroup adds a sink tile's partial sums of one key head in split order
+template <typename T>
+__global__ void __launch_bounds__(256) sink_join_kernel(Params p, const float* part_k, const float* part_v) {
+  const int tile = blockIdx.x % p.tiles, hk = blockIdx.x / p.tiles;
+  T* dst = static_cast<T*>(blockIdx.y ? p.dv : p.dk);
+  const float* src = blockIdx.y ? part_v : part_k;
+  Segment sg;
+  if (!dst || !find_segment(p.koff, p.nk, p.qoff, p.nq, p.batch, 1, kSinkCols, tile, &sg, p.sinks)) return;
+  const int end = sg.len < p.sinks ? sg.len : p.sinks, cols = end - sg.tile * kSinkCols;
+  for (int i = threadIdx.x; i < kSinkCols * p.d; i += 256) {
+    const int col = i / p.d, e = i - col * p.d;
+    if (col >= cols) break;
+    float v = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < p.nsplit; ++s)
+      v += src[(((int64_t(s) * p.tiles + tile) * kSinkCols + col) * p.hk + hk) * p.d + e];
+    dst[((sg.begin + sg.tile * kSinkCols + col) * p.hk + hk) * p.d + e] = T(v);
+  }
+}
+
 // what the host decides before a launch
 struct FwdPlan {
   bool few;  // a sample's rows fit one tile of 32 columns (see fwd_kernel)
@@ -1358,11 +1513,12 @@ struct BwdPlan {
   bool q_few;
   int q_tiles, q_split;  // dQ
   int k_tiles, k_split;  // dK and dV
+  int s_tiles, s_split;  // dK and dV of windowed attention's sinks
 };
 
 // the backward pass's regions of the workspace
 struct BwdParts {
-  float *q_sum, *q_mean, *q_err, *k_sum, *v_sum;
+  float *q_sum, *q_mean, *q_err, *k_sum, *v_sum, *sink_k, *sink_v;
   float *top_q, *top_k;
 };
 
@@ -1371,67 +1527,73 @@ template <typename T>
 int launch_fwd(const Params& p, const FwdPlan& f, hipStream_t s);
 template <typename T>
 int launch_bwd(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s);
+// of windowed attention
+template <typename T>
+int launch_win_fwd(const Params& p, const FwdPlan& f, hipStream_t s);
+template <typename T>
+int launch_win_bwd(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s);
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 
-template <typename T, int DP, bool FEW>
+template <typename T, int DP, bool FEW, bool WIN>
 void launch_fwd_tile(const Params& p, hipStream_t s) {
   constexpr int NW = FEW ? 4 : fwd_waves(sizeof(T), DP);
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    fwd_kernel<T, DP, NW, true, FEW><<<grid, NW * 64, 0, s>>>(p);
+    fwd_kernel<T, DP, NW, true, FEW, WIN><<<grid, NW * 64, 0, s>>>(p);
   else
-    fwd_kernel<T, DP, NW, false, FEW><<<grid, NW * 64, 0, s>>>(p);
+    fwd_kernel<T, DP, NW, false, FEW, WIN><<<grid, NW * 64, 0, s>>>(p);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool WIN>
 void launch_fwd_dim(const Params& p, const FwdPlan& f, hipStream_t s) {
   if (f.few)
-    launch_fwd_tile<T, DP, true>(p, s);
+    launch_fwd_tile<T, DP, true, WIN>(p, s);
   else
-    launch_fwd_tile<T, DP, false>(p, s);
+    launch_fwd_tile<T, DP, false, WIN>(p, s);
 }
 
-template <typename T, int DP, bool FEW>
+template <typename T, int DP, bool FEW, bool WIN>
 void launch_dq_tile(const Params& p, hipStream_t s) {
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    dq_kernel<T, DP, 4, true, FEW><<<grid, 256, 0, s>>>(p);
+    dq_kernel<T, DP, 4, true, FEW, WIN><<<grid, 256, 0, s>>>(p);
   else
-    dq_kernel<T, DP, 4, false, FEW><<<grid, 256, 0, s>>>(p);
+    dq_kernel<T, DP, 4, false, FEW, WIN><<<grid, 256, 0, s>>>(p);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool WIN>
 void launch_dq_dim(const Params& p, const BwdPlan& b, hipStream_t s) {
   if (b.q_few)
-    launch_dq_tile<T, DP, true>(p, s);
+    launch_dq_tile<T, DP, true, WIN>(p, s);
   else
-    launch_dq_tile<T, DP, false>(p, s);
+    launch_dq_tile<T, DP, false, WIN>(p, s);
 }
 
-template <typename T, int DP, bool DK, bool DV>
+template <typename T, int DP, bool DK, bool DV, bool WIN, bool SINK>
 void launch_dkv_tile(const Params& p, hipStream_t s) {
+  constexpr int NW = SINK ? kSinkCols / 32 : 4;
   const unsigned grid = xcd_grid(int64_t(p.tiles) * p.hk * p.nsplit);
   if (p.mask)
-    dkv_kernel<T, DP, 4, true, DK, DV><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, NW, true, DK, DV, WIN, SINK><<<grid, NW * 64, 0, s>>>(p);
   else
-    dkv_kernel<T, DP, 4, false, DK, DV><<<grid, 256, 0, s>>>(p);
+    dkv_kernel<T, DP, NW, false, DK, DV, WIN, SINK><<<grid, NW * 64, 0, s>>>(p);
 }
 
 // The sums of both gradients of a 16-bit head of over 96 leave registers for one wave per SIMD only; a pass for each,
 // which forms the scores again, runs with two (dK and dV of 2 x 11.2k rows, 8 heads of 128: 3.3 -> 2.8 ms).
-template <typename T, int DP>
+template <typename T, int DP, bool WIN, bool SINK>
 void launch_dkv_dim(const Params& p, hipStream_t s) {
   if constexpr (sizeof(T) == 4 || DP <= 96) {
     if (p.dk && p.dv) {
-      launch_dkv_tile<T, DP, true, true>(p, s);
+      launch_dkv_tile<T, DP, true, true, WIN, SINK>(p, s);
       return;
     }
   }
-  if (p.dk) launch_dkv_tile<T, DP, true, false>(p, s);
-  if (p.dv) launch_dkv_tile<T, DP, false, true>(p, s);
+  if (p.dk) launch_dkv_tile<T, DP, true, false, WIN, SINK>(p, s);
+  if (p.dv) launch_dkv_tile<T, DP, false, true, WIN, SINK>(p, s);
 }
 
 template <typename T>
@@ -1450,21 +1612,21 @@ void launch_dq_join(const Params& p, hipStream_t s) {
     dq_join_kernel<T, false><<<unsigned((p.nq * p.hq + 3) / 4), 256, 0, s>>>(p);
 }
 
-template <typename T>
+template <typename T, bool WIN = false>
 int launch_fwd_impl(const Params& p, const FwdPlan& f, hipStream_t s) {
   if (p.d <= 32)
-    launch_fwd_dim<T, 32>(p, f, s);
+    launch_fwd_dim<T, 32, WIN>(p, f, s);
   else if (p.d <= 64)
-    launch_fwd_dim<T, 64>(p, f, s);
+    launch_fwd_dim<T, 64, WIN>(p, f, s);
   else if (p.d <= 96)
-    launch_fwd_dim<T, 96>(p, f, s);
+    launch_fwd_dim<T, 96, WIN>(p, f, s);
   else
-    launch_fwd_dim<T, 128>(p, f, s);
+    launch_fwd_dim<T, 128, WIN>(p, f, s);
   if (p.nsplit > 1) launch_fwd_join<T>(p, s);
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;
 }
 
-template <typename T>
+template <typename T, bool WIN = false>
 int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s) {
   if constexpr (kPExp<T> != 0) {
     p.top_q = w.top_q;
@@ -1480,13 +1642,13 @@ int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s
     p.part_b = w.q_mean;
     p.part_e = w.q_err;
     if (p.d <= 32)
-      launch_dq_dim<T, 32>(p, b, s);
+      launch_dq_dim<T, 32, WIN>(p, b, s);
     else if (p.d <= 64)
-      launch_dq_dim<T, 64>(p, b, s);
+      launch_dq_dim<T, 64, WIN>(p, b, s);
     else if (p.d <= 96)
-      launch_dq_dim<T, 96>(p, b, s);
+      launch_dq_dim<T, 96, WIN>(p, b, s);
     else
-      launch_dq_dim<T, 128>(p, b, s);
+      launch_dq_dim<T, 128, WIN>(p, b, s);
     if (p.nsplit > 1) launch_dq_join<T>(p, s);
   }
   if ((p.dk || p.dv) && p.nk > 0) {
@@ -1495,17 +1657,35 @@ int launch_bwd_impl(Params p, const BwdPlan& b, const BwdParts& w, hipStream_t s
     p.part_a = w.k_sum;
     p.part_b = w.v_sum;
     if (p.d <= 32)
-      launch_dkv_dim<T, 32>(p, s);
+      launch_dkv_dim<T, 32, WIN, false>(p, s);
     else if (p.d <= 64)
-      launch_dkv_dim<T, 64>(p, s);
+      launch_dkv_dim<T, 64, WIN, false>(p, s);
     else if (p.d <= 96)
-      launch_dkv_dim<T, 96>(p, s);
+      launch_dkv_dim<T, 96, WIN, false>(p, s);
     else
-      launch_dkv_dim<T, 128>(p, s);
+      launch_dkv_dim<T, 128, WIN, false>(p, s);
     if (p.nsplit > 1) {
       const int64_t n4 = p.nk * p.hk * p.d / 4;
       sum_splits_kernel<T><<<dim3(unsigned((n4 + 63) / 64), 2), 64, 0, s>>>(w.k_sum, w.v_sum, n4, p.nsplit,
                                                                             static_cast<T*>(p.dk), static_cast<T*>(p.dv));
+    }
+    if constexpr (WIN) {
+      if (p.sinks > 0) {
+        p.tiles = b.s_tiles;
+        p.nsplit = b.s_split;
+        p.part_a = w.sink_k;
+        p.part_b = w.sink_v;
+        if (p.d <= 32)
+          launch_dkv_dim<T, 32, WIN, true>(p, s);
+        else if (p.d <= 64)
+          launch_dkv_dim<T, 64, WIN, true>(p, s);
+        else if (p.d <= 96)
+          launch_dkv_dim<T, 96, WIN, true>(p, s);
+        else
+          launch_dkv_dim<T, 128, WIN, true>(p, s);
+        if (p.nsplit > 1)
+          sink_join_kernel<T><<<dim3(unsigned(p.tiles * p.hk), 2), 256, 0, s>>>(p, w.sink_k, w.sink_v);
+      }
     }
   }
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;
