@@ -7,13 +7,17 @@
 //   dx_t = (1 - a_t) D_t  or  D_t,   dgate_t = a_t (1 - a_t) D_t (h_{t-1} - x_t)  or  a_t (1 - a_t) D_t h_{t-1},
 //   dh0 = c of the first row.
 //
-// Both directions compose maps v -> A v + B, which is associative: a thread walks L rows of a 16-byte vector of channels,
-// the CL lanes beside it the neighbouring channels; 256 / CL threads deep the workgroup's tile is joined by shuffles and
-// LDS, and tiles are joined over the launch.  A sample's first row has A = 0, and A = 0 drops whatever came before it, so
-// samples never touch each other, not even through an infinity or a NaN.
+// Both directions compose maps v -> A v + B, which is associative.  A thread walks L rows of four channels, CL lanes beside
+// it the neighbouring channels, and the 256 / CL threads along the rows are joined by shuffles and LDS: a tile of
+// 256 L / CL rows by 4 CL channels, read once.  Tiles are joined as they run: each publishes its map, takes the value
+// behind the tile kReach before it and the maps of those between, and publishes the value behind itself.  Which words a
+// tile takes is fixed, so sums have one order and results repeat.  Tiles take their numbers from a counter in the order
+// they start: a tile only waits for tiles that run already and that never wait for it.  A published word is its own flag:
+// it was cleared to all ones, a NaN that no result is given, and is written once, so no order between words matters.
 //
-// States, products and sums are fp32.  The backward pass forms h again from the inputs and the states at the tiles'
-// borders, which the forward pass hands out, so y is not read and its rounding does not matter.
+// A sample's first row has A = 0, and A = 0 drops whatever came before it, so samples never touch each other, not even
+// through an infinity or a NaN.  States, products and sums are fp32.  The backward pass forms h again from the inputs and
+// the values at the tiles' borders, which the forward pass hands out: y is not read and its rounding does not matter.
 
 #include <hip/hip_runtime.h>
 
@@ -25,7 +29,8 @@ namespace ssc {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kScanRows = 8;  // rows a thread walks
+constexpr int kReach = 16;   // tiles that a tile looks back over
+constexpr int kFour = 4;     // channels of a thread
 
 struct ScanParams {
   const void *x, *gate, *dy;
@@ -33,9 +38,10 @@ struct ScanParams {
   const int32_t* off;
   const float *h0, *dlast;
   float *last, *dh0;
-  float* carries;  // [tiles][C]: h before each tile's first row
-  float2* agg;     // [tiles][C]: a tile's map (A, B)
-  float* back;     // [tiles][C], backward: c behind each tile's last row
+  const float* carries;  // backward: [tiles][C] h before each tile's first row
+  uint32_t* ticket;
+  uint64_t* maps;        // [tiles][C], by the order of work: a tile's map, A in the low word
+  uint32_t* values;      // [tiles][C], by the order of work: the value that reaches the tile
   int64_t n, x_row, gate_row;
   int32_t c, batch, tiles, groups, rev;
 };
@@ -87,22 +93,80 @@ __device__ __forceinline__ float keep_of(float side) {
   return int(__float_as_uint(side)) < 0 ? 1.f - q : q;
 }
 
+// Ends the compiler's knowledge of a register's value at no instruction: what is formed from it is then formed again in
+// the next walk over the rows, instead of being held from one to the next in twice the registers.
+__device__ __forceinline__ void afresh(float& f) { asm("" : "+v"(f)); }
+__device__ __forceinline__ void afresh(uint2& r) { asm("" : "+v"(r.x), "+v"(r.y)); }
+__device__ __forceinline__ void afresh(float4& r) { asm("" : "+v"(r.x), "+v"(r.y), "+v"(r.z), "+v"(r.w)); }
+
 // The map (A, B) of a value, and its factor after an earlier map's: A = 0 drops what came before, a NaN among it too
 __device__ __forceinline__ float after(float A, float B, float v) { return A == 0.f ? B : fmaf(A, v, B); }
 __device__ __forceinline__ float times(float A, float a) { return A == 0.f ? 0.f : A * a; }
 
-template <int CL, int V>
+// four elements of a row
+template <typename T>
+struct Four {
+  typedef uint2 raw;
+  __device__ static __forceinline__ raw none() { return make_uint2(0, 0); }
+  __device__ static __forceinline__ void unpack(const raw& r, float (&f)[4]) {
+    const uint32_t w[2] = {r.x, r.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (__is_same(T, __bf16)) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        f[2 * i] = float(__builtin_bit_cast(_Float16, uint16_t(w[i] & 0xffffu)));
+        f[2 * i + 1] = float(__builtin_bit_cast(_Float16, uint16_t(w[i] >> 16)));
+      }
+    }
+  }
+  __device__ static __forceinline__ raw pack(const float (&f)[4]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x2 p{f[2 * i], f[2 * i + 1]};
+      if constexpr (__is_same(T, __bf16))
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+      else
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
+    }
+    return make_uint2(w[0], w[1]);
+  }
+};
+template <>
+struct Four<float> {
+  typedef float4 raw;
+  __device__ static __forceinline__ raw none() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ static __forceinline__ void unpack(const raw& r, float (&f)[4]) {
+    f[0] = r.x;
+    f[1] = r.y;
+    f[2] = r.z;
+    f[3] = r.w;
+  }
+  __device__ static __forceinline__ raw pack(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+
+__device__ __forceinline__ void load_state(const float* src, float (&f)[4]) {
+  Four<float>::unpack(*reinterpret_cast<const float4*>(src), f);
+}
+__device__ __forceinline__ void store_state(float* dst, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+}
+
+// The threads' maps of a tile: 256 / CL threads along the rows, 4 CL channels
+template <int CL>
 struct Tile {
-  static constexpr int kChunks = 256 / CL, kRows = kChunks * kScanRows;
+  static constexpr int kCh = 4 * CL;
   // Joins the threads' maps along the rows (BACK: against them): on return (A, B) is the map of the wave's threads before
   // this one, and tot holds each wave's.
   template <bool BACK>
-  __device__ static __forceinline__ void join(float (&A)[V], float (&B)[V], float (*tot)[2][CL * V]) {
+  __device__ static __forceinline__ void join(float (&A)[4], float (&B)[4], float (*tot)[2][kCh]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = threadIdx.x % CL;
 #pragma unroll
     for (int d = CL; d < 64; d <<= 1)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+      for (int v = 0; v < 4; ++v) {
         const float a = BACK ? __shfl_down(A[v], d) : __shfl_up(A[v], d);
         const float b = BACK ? __shfl_down(B[v], d) : __shfl_up(B[v], d);
         if (BACK ? lane + d < 64 : lane >= d) {
@@ -110,14 +174,12 @@ struct Tile {
           A[v] = times(A[v], a);
         }
       }
-    if (BACK ? lane < CL : lane >= 64 - CL)
+    if (BACK ? lane < CL : lane >= 64 - CL) {
+      store_state(&tot[wave][0][col * 4], A);
+      store_state(&tot[wave][1][col * 4], B);
+    }
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        tot[wave][0][col * V + v] = A[v];
-        tot[wave][1][col * V + v] = B[v];
-      }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < 4; ++v) {
       const float a = BACK ? __shfl_down(A[v], CL) : __shfl_up(A[v], CL);
       const float b = BACK ? __shfl_down(B[v], CL) : __shfl_up(B[v], CL);
       const bool some = BACK ? lane + CL < 64 : lane >= CL;
@@ -127,53 +189,121 @@ struct Tile {
   }
   // the value that reaches this thread's rows, from what reaches the tile
   template <bool BACK>
-  __device__ static __forceinline__ void enter(float (&v)[V], const float (&A)[V], const float (&B)[V],
-                                               const float (*tot)[2][CL * V]) {
+  __device__ static __forceinline__ void enter(float (&v)[4], const float (&A)[4], const float (&B)[4],
+                                               const float (*tot)[2][kCh]) {
     const int wave = threadIdx.x >> 6, col = threadIdx.x % CL;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       const int w = BACK ? 3 - i : i;
-      if (BACK ? w > wave : w < wave)
+      if (BACK ? w > wave : w < wave) {
+        float a[4], b[4];
+        load_state(&tot[w][0][col * 4], a);
+        load_state(&tot[w][1][col * 4], b);
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = after(tot[w][0][col * V + k], tot[w][1][col * V + k], v[k]);
+        for (int k = 0; k < 4; ++k) v[k] = after(a[k], b[k], v[k]);
+      }
     }
 #pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = after(A[k], B[k], v[k]);
+    for (int k = 0; k < 4; ++k) v[k] = after(A[k], B[k], v[k]);
   }
-  // the whole tile's map, channel by channel
+  // one channel's map of the whole tile
   template <bool BACK>
-  __device__ static __forceinline__ float2 whole(const float (*tot)[2][CL * V], int ch) {
-    float A = 1.f, B = 0.f;
+  __device__ static __forceinline__ void whole(const float (*tot)[2][kCh], int ch, float* A, float* B) {
+    *A = 1.f;
+    *B = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int w = BACK ? 3 - i : i;
       const float a = tot[w][0][ch], b = tot[w][1][ch];
-      B = after(a, b, B);
-      A = times(a, A);
+      *B = after(a, b, *B);
+      *A = times(a, *A);
     }
-    return make_float2(A, B);
   }
 };
 
-template <int V>
-__device__ __forceinline__ void load_state(const float* src, float (&f)[V]) {
-#pragma unroll
-  for (int v = 0; v < V; v += 4) {
-    const float4 q = *reinterpret_cast<const float4*>(src + v);
-    f[v] = q.x;
-    f[v + 1] = q.y;
-    f[v + 2] = q.z;
-    f[v + 3] = q.w;
-  }
+// Words on their way between tiles
+constexpr uint32_t kNotYet = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t word_of(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u == kNotYet ? 0x7FC00000u : u;
 }
-template <int V>
-__device__ __forceinline__ void store_state(float* dst, const float (&f)[V]) {
+
+// The value that reaches tile `order` (of the order of work): per channel, a lane of each wave composes four of the maps
+// of tiles order - kReach .. order - 1 (the first one the value behind its tile), LDS joins the waves, and the first
+// wave publishes the value behind this tile.  `link` [4][2][4 CL].  Returns the thread's own channels' value in v.
+template <int CL, bool BACK>
+__device__ __forceinline__ void look_back(const ScanParams& p, int order, int group, const float (*tot)[2][4 * CL],
+                                          float (*link)[2][4 * CL], float (&v)[4]) {
+  constexpr int CH = 4 * CL, K = kReach / 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = group * CH + lane;
+  const bool here = lane < CH && ch < p.c;
+  float mA = 1.f, mB = 0.f;
+  if (wave == 0 && here) {
+    Tile<CL>::template whole<BACK>(tot, lane, &mA, &mB);
+    __hip_atomic_store(p.maps + int64_t(order) * p.c + ch, uint64_t(__float_as_uint(mB)) << 32 | word_of(mA), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+  }
+  float A = 1.f, B = 0.f;
+  if (here) {
+    const int first = order - kReach + wave * K;
+    uint64_t w[K];
+    bool done;
+    do {
+      done = true;
 #pragma unroll
-  for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(dst + v) = make_float4(f[v], f[v + 1], f[v + 2], f[v + 3]);
+      for (int k = 0; k < K; ++k) {
+        const int t = first + k;
+        if (t < 0)
+          w[k] = uint64_t(__float_as_uint(1.f));  // no tile: the value stays
+        else if (wave == 0 && k == 0)
+          w[k] = uint64_t(__hip_atomic_load(p.values + int64_t(t + 1) * p.c + ch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) << 32;
+        else
+          w[k] = __hip_atomic_load(p.maps + int64_t(t) * p.c + ch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        done &= (wave == 0 && k == 0 && first >= 0 ? uint32_t(w[k] >> 32) : uint32_t(w[k])) != kNotYet;
+      if (!done) __builtin_amdgcn_s_sleep(1);
+    } while (!done);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float a = __uint_as_float(uint32_t(w[k])), b = __uint_as_float(uint32_t(w[k] >> 32));
+      B = after(a, b, B);
+      A = times(a, A);
+    }
+    link[wave][0][lane] = A;
+    link[wave][1][lane] = B;
+  }
+  __syncthreads();
+  if (wave == 0 && here && order + 1 < p.tiles) {
+    float f = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) f = after(link[w][0][lane], link[w][1][lane], f);
+    __hip_atomic_store(p.values + int64_t(order + 1) * p.c + ch, word_of(after(mA, mB, f)), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+  }
+  const int col = threadIdx.x % CL;
+  if (group * CH + col * 4 < p.c)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float a[4], b[4];
+      load_state(&link[w][0][col * 4], a);
+      load_state(&link[w][1][col * 4], b);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = after(a[k], b[k], v[k]);
+    }
+}
+
+// The tile's number in the order of work, for all threads
+__device__ __forceinline__ int take_ticket(const ScanParams& p, int* slot) {
+  if (p.tiles == 1) return int(blockIdx.x);
+  if (threadIdx.x == 0) *slot = int(__hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  __syncthreads();
+  return *slot;
 }
 
 // Samples with no rows hand on the state (or its gradient) that reaches them; the tiles share them out.
-template <int CL, int V>
+template <int CL>
 __device__ __forceinline__ void empty_samples(const ScanParams& p, int tile, int c0, bool mine, const float* from, float* to) {
   constexpr int CH = 256 / CL;
   if (!to || !mine) return;
@@ -182,271 +312,249 @@ __device__ __forceinline__ void empty_samples(const ScanParams& p, int tile, int
     begin = begin < 0 ? 0 : begin;
     end = end > p.n ? int(p.n) : end;
     if (begin < end) continue;
-    float f[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = 0.f;
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
     if (from) load_state(from + b * p.c + c0, f);
     store_state(to + b * p.c + c0, f);
   }
 }
 
-// SUM: only the tile's map is formed (to p.agg).  Otherwise y and the final states, from the states in p.carries.
-template <typename T, int CL, bool MIX, bool SUM>
+template <typename T, int CL, int L, bool MIX>
 __global__ void __launch_bounds__(256, 2) scan_fwd(ScanParams p) {
-  constexpr int V = Vec<T>::N, L = kScanRows;
-  using TL = Tile<CL, V>;
-  __shared__ int info[TL::kRows];
-  __shared__ float tot[4][2][CL * V];
-  const int group = blockIdx.x % p.groups, tile = blockIdx.x / p.groups;
-  const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * V;
+  using TL = Tile<CL>;
+  using F = Four<T>;
+  constexpr int kRows = 256 / CL * L;
+  __shared__ __align__(16) int info[kRows];
+  __shared__ __align__(16) float tot[4][2][4 * CL], link[4][2][4 * CL];
+  __shared__ int slot;
+  const int work = take_ticket(p, &slot), group = work % p.groups, tile = work / p.groups;
+  const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * 4;
   const bool mine = c0 < p.c;
-  const int64_t t0 = int64_t(tile) * TL::kRows + chunk * L;
-  u32x4 xv[L], gv[L];
+  const int64_t t0 = int64_t(tile) * kRows + chunk * L;
+  const int step = p.rev ? -1 : 1;
+  const int64_t row0 = p.rev ? p.n - 1 - t0 : t0;
+  const int rows = !mine || t0 >= p.n ? 0 : (p.n - t0 < L ? int(p.n - t0) : L);
+  typename F::raw xv[L], gv[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    xv[i] = gv[i] = u32x4{0, 0, 0, 0};
-    if (mine && t0 + i < p.n) {
-      const int64_t row = p.rev ? p.n - 1 - (t0 + i) : t0 + i;
-      xv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.x) + row * p.x_row + c0);
-      gv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.gate) + row * p.gate_row + c0);
+    xv[i] = gv[i] = F::none();
+    if (i < rows) {
+      xv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.x) + (row0 + i * step) * p.x_row + c0);
+      gv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.gate) + (row0 + i * step) * p.gate_row + c0);
     }
   }
-  for (int r = threadIdx.x; r < TL::kRows; r += 256) info[r] = row_info(p, int64_t(tile) * TL::kRows + r);
+  for (int r = threadIdx.x; r < kRows; r += 256) info[r] = row_info(p, int64_t(tile) * kRows + r);
   __syncthreads();
-
-  float a[L][V], b[L][V], A[V], B[V];
+  int any = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.f, B[v] = 0.f;
+  for (int i = 0; i < L; ++i) any |= info[chunk * L + i];
+  const bool plain = !__any((any & 3) != 0);  // no row of the wave begins or ends a sample, or is of none
+
+  float side[L][4], A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
+  // row i's map applied to h
+  auto step_row = [&](int i, float (&h)[4], int what) {
+    float x[4];
+    F::unpack(xv[i], x);
+    if (!plain && what == kNone) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) h[v] = 0.f;
+      return;
+    }
+    if (!plain && (what & kFirst)) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) h[v] = 0.f;
+      if (p.h0 && mine) load_state(p.h0 + int64_t(what >> 2) * p.c + c0, h);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[v] = fmaf(decay_of(side[i][v]), h[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
+  };
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const int what = info[chunk * L + i];
-    float g[V], x[V];
-    Vec<T>::unpack(gv[i], g);
-    Vec<T>::unpack(xv[i], x);
+    float g[4];
+    F::unpack(gv[i], g);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float side = gate_side<T>(g[v]);
-      a[i][v] = decay_of(side);
-      b[i][v] = MIX ? keep_of(side) * x[v] : x[v];
-    }
-    if (what == kNone || (what & kFirst)) {
-      float h[V];
+    for (int v = 0; v < 4; ++v) side[i][v] = gate_side<T>(g[v]);
+    const int what = plain ? 0 : info[chunk * L + i];
+    step_row(i, B, what);
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = 0.f;
-      if (what != kNone && p.h0 && mine) load_state(p.h0 + int64_t(what >> 2) * p.c + c0, h);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        b[i][v] = what == kNone ? 0.f : (p.h0 ? fmaf(a[i][v], h[v], b[i][v]) : b[i][v]);
-        a[i][v] = 0.f;
-        A[v] = 0.f;
-        B[v] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      B[v] = fmaf(a[i][v], B[v], b[i][v]);
-      A[v] *= a[i][v];
-    }
+    for (int v = 0; v < 4; ++v) A[v] = !plain && (what == kNone || (what & kFirst)) ? 0.f : times(A[v], decay_of(side[i][v]));
   }
   TL::template join<false>(A, B, tot);
   __syncthreads();
-  if constexpr (SUM) {
-    for (int ch = threadIdx.x; ch < CL * V; ch += 256) {
-      const int c = group * CL * V + ch;
-      if (c < p.c) p.agg[int64_t(tile) * p.c + c] = TL::template whole<false>(tot, ch);
-    }
-  } else {
-    empty_samples<CL, V>(p, tile, c0, mine, p.h0, p.last);
-    float h[V];
+  empty_samples<CL>(p, tile, c0, mine, p.h0, p.last);
+  float h[4] = {0.f, 0.f, 0.f, 0.f};
+  if (tile == 0 && chunk == 0 && mine) store_state(reinterpret_cast<float*>(p.values) + c0, h);  // no tile waits for it
+  if (p.tiles > 1) look_back<CL, false>(p, tile, group, tot, link, h);
+  TL::template enter<false>(h, A, B, tot);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.f;
-    if (p.tiles > 1 && mine) load_state(p.carries + int64_t(tile) * p.c + c0, h);
-    TL::template enter<false>(h, A, B, tot);
+  for (int i = 0; i < L; ++i) {
+    const int what = plain ? 0 : info[chunk * L + i];
+    afresh(xv[i]);
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const int what = info[chunk * L + i];
-      if (what == kNone || (what & kFirst))
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b[i][v]);
-      if (!mine || t0 + i >= p.n) continue;
-      const int64_t row = p.rev ? p.n - 1 - (t0 + i) : t0 + i;
-      *reinterpret_cast<u32x4*>(static_cast<T*>(p.y) + row * p.c + c0) = Vec<T>::pack(h);
-      if (what != kNone && (what & kLast)) store_state(p.last + int64_t(what >> 2) * p.c + c0, h);
-    }
+    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
+    step_row(i, h, what);
+    if (i >= rows) continue;
+    *reinterpret_cast<typename F::raw*>(static_cast<T*>(p.y) + (row0 + i * step) * p.c + c0) = F::pack(h);
+    if (!plain && what != kNone && (what & kLast)) store_state(p.last + int64_t(what >> 2) * p.c + c0, h);
   }
 }
 
-// SUM: the tile's map of c (from its end to its beginning) to p.agg.  Otherwise the gradients, from the states in
-// p.carries and the c in p.back.
-template <typename T, int CL, bool MIX, bool SUM>
+template <typename T, int CL, int L, bool MIX>
 __global__ void __launch_bounds__(256, 2) scan_bwd(ScanParams p) {
-  constexpr int V = Vec<T>::N, L = kScanRows;
-  using TL = Tile<CL, V>;
-  __shared__ int info[TL::kRows];
-  __shared__ float tot[4][2][CL * V], totb[4][2][CL * V];
-  const int group = blockIdx.x % p.groups, tile = blockIdx.x / p.groups;
-  const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * V;
+  using TL = Tile<CL>;
+  using F = Four<T>;
+  constexpr int kRows = 256 / CL * L;
+  __shared__ __align__(16) int info[kRows];
+  __shared__ __align__(16) float tot[4][2][4 * CL], totb[4][2][4 * CL], link[4][2][4 * CL];
+  __shared__ int slot;
+  const int work = take_ticket(p, &slot), group = work % p.groups, order = work / p.groups, tile = p.tiles - 1 - order;
+  const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * 4;
   const bool mine = c0 < p.c;
-  const int64_t t0 = int64_t(tile) * TL::kRows + chunk * L;
-  u32x4 xv[SUM ? 1 : L], gv[L], uv[L];
+  const int64_t t0 = int64_t(tile) * kRows + chunk * L;
+  const int step = p.rev ? -1 : 1;
+  const int64_t row0 = p.rev ? p.n - 1 - t0 : t0;
+  const int rows = !mine || t0 >= p.n ? 0 : (p.n - t0 < L ? int(p.n - t0) : L);
+  typename F::raw xv[L], gv[L], uv[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    gv[i] = uv[i] = u32x4{0, 0, 0, 0};
-    if constexpr (!SUM) xv[i] = u32x4{0, 0, 0, 0};
-    if (mine && t0 + i < p.n) {
-      const int64_t row = p.rev ? p.n - 1 - (t0 + i) : t0 + i;
-      gv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.gate) + row * p.gate_row + c0);
-      uv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.dy) + row * p.c + c0);
-      if constexpr (!SUM) xv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.x) + row * p.x_row + c0);
+    xv[i] = gv[i] = uv[i] = F::none();
+    if (i < rows) {
+      gv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.gate) + (row0 + i * step) * p.gate_row + c0);
+      uv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.dy) + (row0 + i * step) * p.c + c0);
+      xv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.x) + (row0 + i * step) * p.x_row + c0);
     }
   }
-  for (int r = threadIdx.x; r < TL::kRows; r += 256) info[r] = row_info(p, int64_t(tile) * TL::kRows + r);
+  float h[4] = {0.f, 0.f, 0.f, 0.f};
+  if (tile > 0 && mine) load_state(p.carries + int64_t(tile) * p.c + c0, h);
+  for (int r = threadIdx.x; r < kRows; r += 256) info[r] = row_info(p, int64_t(tile) * kRows + r);
   __syncthreads();
+  int any = 0;
+#pragma unroll
+  for (int i = 0; i < L; ++i) any |= info[chunk * L + i];
+  const bool plain = !__any((any & 3) != 0);
 
-  float side[L][V], u[SUM ? 1 : L][V], A[V], B[V];
+  float side[L][4], u[L][4];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    float g[V];
-    Vec<T>::unpack(gv[i], g);
+    float g[4];
+    F::unpack(gv[i], g);
 #pragma unroll
-    for (int v = 0; v < V; ++v) side[i][v] = gate_side<T>(g[v]);
+    for (int v = 0; v < 4; ++v) side[i][v] = gate_side<T>(g[v]);
   }
-  // what a row adds to c where the sample ends with it
-  auto end_of = [&](int what, float (&f)[V]) {
+  // the value that a sample's first row (its last one, in the other direction) begins with
+  auto begin = [&](const float* from, int what, float (&f)[4]) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = 0.f;
-    if (what != kNone && p.dlast && mine) load_state(p.dlast + int64_t(what >> 2) * p.c + c0, f);
+    for (int v = 0; v < 4; ++v) f[v] = 0.f;
+    if (what != kNone && from && mine) load_state(from + int64_t(what >> 2) * p.c + c0, f);
   };
-  float Ab[V], Bb[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) Ab[v] = 1.f, Bb[v] = 0.f;
+  float A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
+  float Ab[4] = {1.f, 1.f, 1.f, 1.f}, Bb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = L - 1; i >= 0; --i) {
-    const int what = info[chunk * L + i];
-    float dy[V];
-    Vec<T>::unpack(uv[i], dy);
-    if (what == kNone || (what & kLast)) {
-      end_of(what, Bb);
+    const int what = plain ? 0 : info[chunk * L + i];
+    const bool cut = !plain && (what == kNone || (what & kLast));
+    float dy[4];
+    F::unpack(uv[i], dy);
+    if (cut) begin(p.dlast, what, Bb);
 #pragma unroll
-      for (int v = 0; v < V; ++v) Ab[v] = 0.f;
+    for (int v = 0; v < 4; ++v) {
+      const float a = decay_of(side[i][v]);
+      Bb[v] = !plain && what == kNone ? 0.f : a * (dy[v] + Bb[v]);
+      Ab[v] = cut ? 0.f : times(Ab[v], a);
     }
+  }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float a = what == kNone ? 0.f : decay_of(side[i][v]);
-      Bb[v] = what == kNone ? 0.f : a * (dy[v] + Bb[v]);
-      Ab[v] *= a;
+  for (int i = 0; i < L; ++i) {
+    const int what = plain ? 0 : info[chunk * L + i];
+    const bool cut = !plain && (what == kNone || (what & kFirst));
+    float x[4];
+    F::unpack(xv[i], x);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
+    if (cut) begin(p.h0, what, B);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float a = decay_of(side[i][v]);
+      B[v] = !plain && what == kNone ? 0.f : fmaf(a, B[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
+      A[v] = cut ? 0.f : times(A[v], a);
     }
   }
   TL::template join<true>(Ab, Bb, totb);
-  if constexpr (SUM) {
-    __syncthreads();
-    for (int ch = threadIdx.x; ch < CL * V; ch += 256) {
-      const int c = group * CL * V + ch;
-      if (c < p.c) p.agg[int64_t(tile) * p.c + c] = TL::template whole<true>(totb, ch);
+  TL::template join<false>(A, B, tot);
+  __syncthreads();
+  empty_samples<CL>(p, tile, c0, mine, p.dlast, p.dh0);
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.tiles > 1) look_back<CL, true>(p, order, group, totb, link, c);
+  TL::template enter<false>(h, A, B, tot);
+  TL::template enter<true>(c, Ab, Bb, totb);
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int what = plain ? 0 : info[chunk * L + i];
+    float x[4];
+    afresh(xv[i]);
+    F::unpack(xv[i], x);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
+    if (!plain && (what == kNone || (what & kFirst))) begin(p.h0, what, h);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      u[i][v] = MIX ? h[v] - x[v] : h[v];
+      h[v] = !plain && what == kNone ? 0.f : fmaf(decay_of(side[i][v]), h[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
     }
-  } else {
-    // the states again
+  }
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, B[v] = 0.f;
-    auto first_of = [&](int what, float (&f)[V]) {
+  for (int i = L - 1; i >= 0; --i) {
+    const int what = plain ? 0 : info[chunk * L + i];
+    const bool none = !plain && what == kNone;
+    float dy[4], dx[4], dg[4];
+    afresh(uv[i]);
+    F::unpack(uv[i], dy);
 #pragma unroll
-      for (int v = 0; v < V; ++v) f[v] = 0.f;
-      if (what != kNone && p.h0 && mine) load_state(p.h0 + int64_t(what >> 2) * p.c + c0, f);
-    };
+    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
+    if (!plain && (none || (what & kLast))) begin(p.dlast, what, c);
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const int what = info[chunk * L + i];
-      float x[V];
-      Vec<T>::unpack(xv[i], x);
-      if (what == kNone || (what & kFirst)) {
-        first_of(what, B);
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 0.f;
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float a = what == kNone ? 0.f : decay_of(side[i][v]);
-        B[v] = what == kNone ? 0.f : fmaf(a, B[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
-        A[v] *= a;
-      }
+    for (int v = 0; v < 4; ++v) {
+      const float q = fabsf(side[i][v]), d = dy[v] + c[v];
+      dx[v] = none ? 0.f : (MIX ? keep_of(side[i][v]) * d : d);
+      dg[v] = none ? 0.f : q * (1.f - q) * d * u[i][v];
+      c[v] = none ? 0.f : decay_of(side[i][v]) * d;
     }
-    TL::template join<false>(A, B, tot);
-    __syncthreads();
-    empty_samples<CL, V>(p, tile, c0, mine, p.dlast, p.dh0);
-    float h[V], c[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = c[v] = 0.f;
-    if (p.tiles > 1 && mine) {
-      load_state(p.carries + int64_t(tile) * p.c + c0, h);
-      load_state(p.back + int64_t(tile) * p.c + c0, c);
-    }
-    TL::template enter<false>(h, A, B, tot);
-    TL::template enter<true>(c, Ab, Bb, totb);
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const int what = info[chunk * L + i];
-      float x[V];
-      Vec<T>::unpack(xv[i], x);
-      if (what == kNone || (what & kFirst)) first_of(what, h);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        u[i][v] = MIX ? h[v] - x[v] : h[v];
-        h[v] = what == kNone ? 0.f : fmaf(decay_of(side[i][v]), h[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
-      }
-    }
-#pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-      const int what = info[chunk * L + i];
-      float dy[V], dx[V], dg[V];
-      Vec<T>::unpack(uv[i], dy);
-      if (what == kNone || (what & kLast)) end_of(what, c);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float q = fabsf(side[i][v]), d = dy[v] + c[v];
-        dx[v] = what == kNone ? 0.f : (MIX ? keep_of(side[i][v]) * d : d);
-        dg[v] = what == kNone ? 0.f : q * (1.f - q) * d * u[i][v];
-        c[v] = decay_of(side[i][v]) * d;
-      }
-      if (!mine || t0 + i >= p.n) continue;
-      const int64_t row = p.rev ? p.n - 1 - (t0 + i) : t0 + i;
-      *reinterpret_cast<u32x4*>(static_cast<T*>(p.dx) + row * p.c + c0) = Vec<T>::pack(dx);
-      *reinterpret_cast<u32x4*>(static_cast<T*>(p.dgate) + row * p.c + c0) = Vec<T>::pack(dg);
-      if (p.dh0 && what != kNone && (what & kFirst)) store_state(p.dh0 + int64_t(what >> 2) * p.c + c0, c);
-    }
+    if (i >= rows) continue;
+    const int64_t at = (row0 + i * step) * p.c + c0;
+    *reinterpret_cast<typename F::raw*>(static_cast<T*>(p.dx) + at) = F::pack(dx);
+    *reinterpret_cast<typename F::raw*>(static_cast<T*>(p.dgate) + at) = F::pack(dg);
+    if (!plain && !none && (what & kFirst) && p.dh0) store_state(p.dh0 + int64_t(what >> 2) * p.c + c0, c);
   }
 }
 
-// What reaches each tile, from the tiles' maps: a thread a channel
-template <bool BACK>
-__global__ void __launch_bounds__(64) scan_tiles(const float2* agg, float* into, int tiles, int c) {
-  const int ch = blockIdx.x * 64 + threadIdx.x;
-  if (ch >= c) return;
-  float v = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < tiles; ++i) {
-    const int64_t at = int64_t(BACK ? tiles - 1 - i : i) * c + ch;
-    into[at] = v;
-    const float2 m = agg[at];
-    v = after(m.x, m.y, v);
-  }
+// Clears the words between tiles (counted in 16-byte pieces) and the counter
+__global__ void __launch_bounds__(256) scan_clear(uint4* maps, int64_t nmaps, uint4* values, int64_t nvalues, uint32_t* ticket) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const uint4 none = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
+  if (i < nmaps) maps[i] = none;
+  if (i < nvalues) values[i] = none;
+  if (i == 0) *ticket = 0;
 }
 
 int esize(int32_t dtype) { return dtype == SSC_F32 ? 4 : 2; }
 bool bad(const void* ptr) { return !ptr || !aligned16(ptr); }
 
+// Rows of a thread, lanes of a tile's row, tiles along the rows and groups of channels
 struct ScanPlan {
-  int lanes;  // a row's vectors side by side in a workgroup
+  int rows, lanes;
   int64_t tiles, groups;
 };
 ScanPlan scan_plan(const ssc_scan_shape& a) {
-  const int vecs = a.channels * esize(a.dtype) / 16;
+  const int vecs = a.channels / kFour;
   ScanPlan s{};
-  s.lanes = vecs <= 4 ? 4 : (vecs <= 8 ? 8 : 16);
-  const int64_t rows = int64_t(256 / s.lanes) * kScanRows;
-  s.tiles = a.n > 0 ? (a.n + rows - 1) / rows : 1;
+  s.lanes = vecs <= 8 ? 8 : 16;
+  s.rows = a.dtype == SSC_F32 ? 8 : 16;
   s.groups = (vecs + s.lanes - 1) / s.lanes;
+  auto tiles = [&]() {
+    const int64_t rows = int64_t(256 / s.lanes) * s.rows;
+    return a.n > 0 ? (a.n + rows - 1) / rows : 1;
+  };
+  if (tiles() * s.groups < 512) s.rows = 4;
+  s.tiles = tiles();
   return s;
 }
 
@@ -484,62 +592,63 @@ size_t carry_bytes(const ssc_scan_shape& a) {
 }
 
 struct ScanWs {
-  size_t agg = 0, into = 0, total = 0;
+  size_t maps = 256, values = 0, total = 0;  // the counter lies first
 };
 ScanWs scan_ws(const ssc_scan_shape& a) {
   const size_t n = align_up(carry_bytes(a), 256);
   ScanWs w;
-  w.into = 2 * n;
-  w.total = 3 * n;
+  w.values = w.maps + 2 * n;
+  w.total = w.values + n;
   return w;
 }
 
-template <typename T, int CL, bool MIX>
-void scan_launch(const ScanParams& p, bool back, hipStream_t s) {
-  const unsigned grid = unsigned(int64_t(p.tiles) * p.groups), per = unsigned((p.c + 63) / 64);
-  if (!back) {
-    if (p.tiles > 1) {
-      scan_fwd<T, CL, MIX, true><<<grid, 256, 0, s>>>(p);
-      scan_tiles<false><<<per, 64, 0, s>>>(p.agg, p.carries, p.tiles, p.c);
-    }
-    scan_fwd<T, CL, MIX, false><<<grid, 256, 0, s>>>(p);
+template <typename T, int CL, int L>
+void scan_launch(const ScanParams& p, bool mix, bool back, hipStream_t s) {
+  const unsigned grid = unsigned(int64_t(p.tiles) * p.groups);
+  if (back) {
+    if (mix)
+      scan_bwd<T, CL, L, true><<<grid, 256, 0, s>>>(p);
+    else
+      scan_bwd<T, CL, L, false><<<grid, 256, 0, s>>>(p);
   } else {
-    if (p.tiles > 1) {
-      scan_bwd<T, CL, MIX, true><<<grid, 256, 0, s>>>(p);
-      scan_tiles<true><<<per, 64, 0, s>>>(p.agg, p.back, p.tiles, p.c);
-    }
-    scan_bwd<T, CL, MIX, false><<<grid, 256, 0, s>>>(p);
+    if (mix)
+      scan_fwd<T, CL, L, true><<<grid, 256, 0, s>>>(p);
+    else
+      scan_fwd<T, CL, L, false><<<grid, 256, 0, s>>>(p);
   }
 }
 
-template <typename T, int CL>
-void scan_form(const ScanParams& p, bool mix, bool back, hipStream_t s) {
-  if (mix)
-    scan_launch<T, CL, true>(p, back, s);
-  else
-    scan_launch<T, CL, false>(p, back, s);
-}
-
 template <typename T>
-void scan_lanes(const ScanParams& p, int lanes, bool mix, bool back, hipStream_t s) {
-  if (lanes == 4)
-    scan_form<T, 4>(p, mix, back, s);
-  else if (lanes == 8)
-    scan_form<T, 8>(p, mix, back, s);
-  else
-    scan_form<T, 16>(p, mix, back, s);
+void scan_form(const ScanPlan& f, const ScanParams& p, bool mix, bool back, hipStream_t s) {
+  constexpr int kRows = sizeof(T) == 4 ? 8 : 16;
+  if (f.lanes == 8) {
+    if (f.rows == 4)
+      scan_launch<T, 8, 4>(p, mix, back, s);
+    else
+      scan_launch<T, 8, kRows>(p, mix, back, s);
+  } else {
+    if (f.rows == 4)
+      scan_launch<T, 16, 4>(p, mix, back, s);
+    else
+      scan_launch<T, 16, kRows>(p, mix, back, s);
+  }
 }
 
 int scan_run(const ssc_scan_shape& a, const ScanPlan& sp, const ScanParams& p, bool back, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool mix = a.form == SSC_SCAN_MIX;
   (void)hipGetLastError();
+  if (p.tiles > 1) {
+    const int64_t words = p.tiles * int64_t(p.c);  // channels come in fours
+    scan_clear<<<unsigned((words / 2 + 255) / 256), 256, 0, s>>>(reinterpret_cast<uint4*>(p.maps), words / 2,
+                                                               reinterpret_cast<uint4*>(p.values), words / 4, p.ticket);
+  }
   if (a.dtype == SSC_F32)
-    scan_lanes<float>(p, sp.lanes, mix, back, s);
+    scan_form<float>(sp, p, mix, back, s);
   else if (a.dtype == SSC_F16)
-    scan_lanes<_Float16>(p, sp.lanes, mix, back, s);
+    scan_form<_Float16>(sp, p, mix, back, s);
   else
-    scan_lanes<__bf16>(p, sp.lanes, mix, back, s);
+    scan_form<__bf16>(sp, p, mix, back, s);
   return hipGetLastError() == hipSuccess ? SSC_OK : SSC_ERR_HIP;
 }
 
@@ -576,8 +685,9 @@ extern "C" int ssc_gated_scan_fwd(const ssc_scan_shape* shape, const void* x, co
   p.h0 = h0;
   p.y = y;
   p.last = last;
-  p.agg = reinterpret_cast<float2*>(ws + w.agg);
-  p.carries = carries ? carries : reinterpret_cast<float*>(ws + w.into);
+  p.ticket = reinterpret_cast<uint32_t*>(ws);
+  p.maps = reinterpret_cast<uint64_t*>(ws + w.maps);
+  p.values = carries ? reinterpret_cast<uint32_t*>(carries) : reinterpret_cast<uint32_t*>(ws + w.values);
   return scan_run(a, sp, p, false, stream);
 }
 
@@ -604,8 +714,9 @@ extern "C" int ssc_gated_scan_bwd(const ssc_scan_shape* shape, const void* x, co
   p.dx = dx;
   p.dgate = dgate;
   p.dh0 = dh0;
-  p.agg = reinterpret_cast<float2*>(ws + w.agg);
-  p.back = reinterpret_cast<float*>(ws + w.into);
-  p.carries = const_cast<float*>(carries);
+  p.ticket = reinterpret_cast<uint32_t*>(ws);
+  p.maps = reinterpret_cast<uint64_t*>(ws + w.maps);
+  p.values = reinterpret_cast<uint32_t*>(ws + w.values);
+  p.carries = carries;
   return scan_run(a, sp, p, true, stream);
 }
