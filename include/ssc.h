@@ -671,12 +671,15 @@ int ssc_dropout(int64_t elements, int32_t dtype, double p, int32_t layer, const 
  * ------------------------------------------------------------------------ */
 enum ssc_scan_form { SSC_SCAN_MIX = 0, SSC_SCAN_SUM = 1 };
 
+/* a tile's 512 rows are addressed with 32-bit byte offsets from its first */
+#define SSC_MAX_SCAN_ROW_STRIDE (1LL << 21)
+
 /* Sizes of a call (a host struct, read during the call). */
 typedef struct ssc_scan_shape {
   int64_t n;                             /* rows, at most SSC_MAX_SEQ_ROWS; a workgroup of 256 threads takes 128 rows of
                                           * 256 bytes (256 of 128, 512 of 64 where the rows are no longer), with fewer
                                           * than 2^32 threads in all */
-  int64_t x_row_stride, gate_row_stride; /* elements, multiples of 16 bytes, not negative */
+  int64_t x_row_stride, gate_row_stride; /* elements, multiples of 16 bytes, 0 .. SSC_MAX_SCAN_ROW_STRIDE */
   int32_t batch;                         /* samples, 1 .. SSC_MAX_ATTN_BATCH */
   int32_t channels;                      /* whole 16-byte vectors, at most SSC_MAX_SEQ_CHANNELS */
   int32_t dtype;

@@ -38,7 +38,7 @@ struct ScanParams {
   const int32_t* off;
   const float *h0, *dlast;
   float *last, *dh0;
-  const float* carries;  // backward: [tiles][C] h before each tile's first row
+  float* carries;        // h before the first row of each tile of the backward pass
   uint32_t* ticket;
   uint64_t* maps;        // [tiles][C], by the order of work: a tile's map, A in the low word
   uint32_t* values;      // [tiles][C], by the order of work: the value that reaches the tile
@@ -69,10 +69,10 @@ __device__ __forceinline__ int row_info(const ScanParams& p, int64_t t) {
   return 4 * lo + (row == first ? kFirst : 0) + (row == last ? kLast : 0);
 }
 
-// sigmoid(g) as its smaller side q in [0, 1/2], with the sign of g: q = e / (1 + e), e = exp(-|g|).  One side of the pair
-// (a, 1 - a) is q and the other 1 - q, so both keep their relative error however near to 0 or 1 they are.
+// a = sigmoid(g) and 1 - a.  The smaller of the two is q = e / (1 + e), e = exp(-|g|), and the other 1 - q: both keep
+// their relative error however near to 0 or 1 they are.
 template <typename T>
-__device__ __forceinline__ float gate_side(float g) {
+__device__ __forceinline__ void sides(float g, float& a, float& keep) {
   float q;
   if constexpr (sizeof(T) == 4) {
     const float e = expf(-fabsf(g));
@@ -82,22 +82,43 @@ __device__ __forceinline__ float gate_side(float g) {
     const float e = __builtin_amdgcn_exp2f(-fabsf(g) * kLog2e);
     q = e * __builtin_amdgcn_rcpf(1.f + e);
   }
-  return __uint_as_float(__float_as_uint(q) | (__float_as_uint(g) & 0x80000000u));
-}
-__device__ __forceinline__ float decay_of(float side) {
-  const float q = fabsf(side);
-  return int(__float_as_uint(side)) < 0 ? q : 1.f - q;
-}
-__device__ __forceinline__ float keep_of(float side) {
-  const float q = fabsf(side);
-  return int(__float_as_uint(side)) < 0 ? 1.f - q : q;
+  const float big = 1.f - q;
+  a = g < 0.f ? q : big;
+  keep = g < 0.f ? big : q;
 }
 
-// Ends the compiler's knowledge of a register's value at no instruction: what is formed from it is then formed again in
-// the next walk over the rows, instead of being held from one to the next in twice the registers.
-__device__ __forceinline__ void afresh(float& f) { asm("" : "+v"(f)); }
+// Ends the compiler's knowledge of a register's value, at no instruction: what is unpacked from it is then unpacked again
+// in the next walk over the rows, instead of being held from one to the next in twice the registers.
 __device__ __forceinline__ void afresh(uint2& r) { asm("" : "+v"(r.x), "+v"(r.y)); }
-__device__ __forceinline__ void afresh(float4& r) { asm("" : "+v"(r.x), "+v"(r.y), "+v"(r.z), "+v"(r.w)); }
+__device__ __forceinline__ void afresh(float4&) {}
+
+// Where a thread's rows of a [n][C] tensor lie: a base that the workgroup shares, which steps from row to row in scalar
+// registers, and the thread's offset from it, which 32 bits hold (row strides are bounded for it).
+struct Lane {
+  const char* base;
+  int64_t step;
+  uint32_t off;
+  // first: the tile's first place; place: the thread's first place in it; rows: the tile's; col: the thread's first channel
+  __device__ __forceinline__ void init(const void* ptr, int64_t row_bytes, const ScanParams& p, int64_t first, int place, int rows,
+                                       int col_bytes) {
+    // reversed, places walk down from the tile's end; its lowest row may lie before row 0, where no place of it is taken
+    const int64_t low = p.rev ? p.n - first - rows : first;
+    base = static_cast<const char*>(ptr) + low * row_bytes;
+    step = p.rev ? -row_bytes : row_bytes;
+    off = uint32_t(p.rev ? rows - 1 - place : place) * uint32_t(row_bytes) + uint32_t(col_bytes);
+  }
+  template <typename R>
+  __device__ __forceinline__ R get(int i) const {
+    return *reinterpret_cast<const R*>(base + i * step + off);
+  }
+  template <typename R>
+  __device__ __forceinline__ void put(int i, const R& v) const {
+    *reinterpret_cast<R*>(const_cast<char*>(base) + i * step + off) = v;
+  }
+};
+
+// a value every lane holds alike, in a scalar register
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // The map (A, B) of a value, and its factor after an earlier map's: A = 0 drops what came before, a NaN among it too
 __device__ __forceinline__ float after(float A, float B, float v) { return A == 0.f ? B : fmaf(A, v, B); }
@@ -299,7 +320,7 @@ __device__ __forceinline__ int take_ticket(const ScanParams& p, int* slot) {
   if (p.tiles == 1) return int(blockIdx.x);
   if (threadIdx.x == 0) *slot = int(__hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
   __syncthreads();
-  return *slot;
+  return uniform(*slot);
 }
 
 // Samples with no rows hand on the state (or its gradient) that reaches them; the tiles share them out.
@@ -318,8 +339,9 @@ __device__ __forceinline__ void empty_samples(const ScanParams& p, int tile, int
   }
 }
 
-template <typename T, int CL, int L, bool MIX>
-__global__ void __launch_bounds__(256, 2) scan_fwd(ScanParams p) {
+// LB: rows of the backward pass's threads, whose tiles are as many times shorter as L is larger
+template <typename T, int CL, int L, int LB, bool MIX>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_fwd(ScanParams p) {
   using TL = Tile<CL>;
   using F = Four<T>;
   constexpr int kRows = 256 / CL * L;
@@ -329,17 +351,29 @@ __global__ void __launch_bounds__(256, 2) scan_fwd(ScanParams p) {
   const int work = take_ticket(p, &slot), group = work % p.groups, tile = work / p.groups;
   const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * 4;
   const bool mine = c0 < p.c;
-  const int64_t t0 = int64_t(tile) * kRows + chunk * L;
-  const int step = p.rev ? -1 : 1;
-  const int64_t row0 = p.rev ? p.n - 1 - t0 : t0;
-  const int rows = !mine || t0 >= p.n ? 0 : (p.n - t0 < L ? int(p.n - t0) : L);
+  const int64_t first = int64_t(tile) * kRows, t0 = first + chunk * L;
+  const bool whole = first + kRows <= p.n;  // every row of the tile exists
+  const int rows = t0 >= p.n ? 0 : (p.n - t0 < L ? int(p.n - t0) : L);
+  // lanes past the last channel compute on the first ones and keep nothing
+  const int col = (mine ? c0 : 0) * int(sizeof(T));
+  Lane xl, gl;
+  xl.init(p.x, p.x_row * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
+  gl.init(p.gate, p.gate_row * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
   typename F::raw xv[L], gv[L];
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    xv[i] = gv[i] = F::none();
-    if (i < rows) {
-      xv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.x) + (row0 + i * step) * p.x_row + c0);
-      gv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.gate) + (row0 + i * step) * p.gate_row + c0);
+    for (int i = 0; i < L; ++i) {
+      xv[i] = xl.get<typename F::raw>(i);
+      gv[i] = gl.get<typename F::raw>(i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      xv[i] = gv[i] = F::none();
+      if (i < rows) {
+        xv[i] = xl.get<typename F::raw>(i);
+        gv[i] = gl.get<typename F::raw>(i);
+      }
     }
   }
   for (int r = threadIdx.x; r < kRows; r += 256) info[r] = row_info(p, int64_t(tile) * kRows + r);
@@ -349,57 +383,68 @@ __global__ void __launch_bounds__(256, 2) scan_fwd(ScanParams p) {
   for (int i = 0; i < L; ++i) any |= info[chunk * L + i];
   const bool plain = !__any((any & 3) != 0);  // no row of the wave begins or ends a sample, or is of none
 
-  float side[L][4], A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
-  // row i's map applied to h
-  auto step_row = [&](int i, float (&h)[4], int what) {
-    float x[4];
-    F::unpack(xv[i], x);
-    if (!plain && what == kNone) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) h[v] = 0.f;
-      return;
-    }
-    if (!plain && (what & kFirst)) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) h[v] = 0.f;
-      if (p.h0 && mine) load_state(p.h0 + int64_t(what >> 2) * p.c + c0, h);
-    }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) h[v] = fmaf(decay_of(side[i][v]), h[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
-  };
+  float a[L][4], b[L][4], A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    float g[4];
+    float g[4], x[4];
     F::unpack(gv[i], g);
+    F::unpack(xv[i], x);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) side[i][v] = gate_side<T>(g[v]);
-    const int what = plain ? 0 : info[chunk * L + i];
-    step_row(i, B, what);
+    for (int v = 0; v < 4; ++v) {
+      float keep;
+      sides<T>(g[v], a[i][v], keep);
+      b[i][v] = MIX ? keep * x[v] : x[v];
+    }
+    if (!plain) {
+      const int what = info[chunk * L + i];
+      if (what & kFirst) {  // kNone has all bits
+        float h[4] = {0.f, 0.f, 0.f, 0.f};
+        if (what != kNone && p.h0 && mine) load_state(p.h0 + int64_t(what >> 2) * p.c + c0, h);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) A[v] = !plain && (what == kNone || (what & kFirst)) ? 0.f : times(A[v], decay_of(side[i][v]));
+        for (int v = 0; v < 4; ++v) {
+          b[i][v] = what == kNone ? 0.f : (p.h0 ? fmaf(a[i][v], h[v], b[i][v]) : b[i][v]);
+          a[i][v] = A[v] = B[v] = 0.f;
+        }
+      }
+    }
+    // a NaN decay makes A one where it should stay 0, but B as well
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      B[v] = fmaf(a[i][v], B[v], b[i][v]);
+      A[v] *= a[i][v];
+    }
   }
   TL::template join<false>(A, B, tot);
   __syncthreads();
   empty_samples<CL>(p, tile, c0, mine, p.h0, p.last);
   float h[4] = {0.f, 0.f, 0.f, 0.f};
-  if (tile == 0 && chunk == 0 && mine) store_state(reinterpret_cast<float*>(p.values) + c0, h);  // no tile waits for it
   if (p.tiles > 1) look_back<CL, false>(p, tile, group, tot, link, h);
   TL::template enter<false>(h, A, B, tot);
+  if (!mine) return;
+  constexpr int kParts = L / LB, kPart = 256 / CL / kParts;
+  if (p.carries && chunk % kPart == 0 && rows > 0)
+    store_state(p.carries + (int64_t(tile) * kParts + chunk / kPart) * p.c + c0, h);
+  Lane yl;
+  yl.init(p.y, p.c * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const int what = plain ? 0 : info[chunk * L + i];
-    afresh(xv[i]);
+    int what = 0;
+    if (!plain) {
+      what = info[chunk * L + i];
+      if (what & kFirst)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
-    step_row(i, h, what);
-    if (i >= rows) continue;
-    *reinterpret_cast<typename F::raw*>(static_cast<T*>(p.y) + (row0 + i * step) * p.c + c0) = F::pack(h);
+        for (int v = 0; v < 4; ++v) h[v] = 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[v] = fmaf(a[i][v], h[v], b[i][v]);
+    if (!whole && i >= rows) break;
+    yl.put(i, F::pack(h));
     if (!plain && what != kNone && (what & kLast)) store_state(p.last + int64_t(what >> 2) * p.c + c0, h);
   }
 }
 
 template <typename T, int CL, int L, bool MIX>
-__global__ void __launch_bounds__(256, 2) scan_bwd(ScanParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanParams p) {
   using TL = Tile<CL>;
   using F = Four<T>;
   constexpr int kRows = 256 / CL * L;
@@ -409,18 +454,31 @@ __global__ void __launch_bounds__(256, 2) scan_bwd(ScanParams p) {
   const int work = take_ticket(p, &slot), group = work % p.groups, order = work / p.groups, tile = p.tiles - 1 - order;
   const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * 4;
   const bool mine = c0 < p.c;
-  const int64_t t0 = int64_t(tile) * kRows + chunk * L;
-  const int step = p.rev ? -1 : 1;
-  const int64_t row0 = p.rev ? p.n - 1 - t0 : t0;
-  const int rows = !mine || t0 >= p.n ? 0 : (p.n - t0 < L ? int(p.n - t0) : L);
+  const int64_t first = int64_t(tile) * kRows, t0 = first + chunk * L;
+  const bool whole = first + kRows <= p.n;
+  const int rows = t0 >= p.n ? 0 : (p.n - t0 < L ? int(p.n - t0) : L);
+  const int col = (mine ? c0 : 0) * int(sizeof(T));
+  Lane xl, gl, ul;
+  xl.init(p.x, p.x_row * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
+  gl.init(p.gate, p.gate_row * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
+  ul.init(p.dy, p.c * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
   typename F::raw xv[L], gv[L], uv[L];
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    xv[i] = gv[i] = uv[i] = F::none();
-    if (i < rows) {
-      gv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.gate) + (row0 + i * step) * p.gate_row + c0);
-      uv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.dy) + (row0 + i * step) * p.c + c0);
-      xv[i] = *reinterpret_cast<const typename F::raw*>(static_cast<const T*>(p.x) + (row0 + i * step) * p.x_row + c0);
+    for (int i = 0; i < L; ++i) {
+      gv[i] = gl.get<typename F::raw>(i);
+      uv[i] = ul.get<typename F::raw>(i);
+      xv[i] = xl.get<typename F::raw>(i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      xv[i] = gv[i] = uv[i] = F::none();
+      if (i < rows) {
+        gv[i] = gl.get<typename F::raw>(i);
+        uv[i] = ul.get<typename F::raw>(i);
+        xv[i] = xl.get<typename F::raw>(i);
+      }
     }
   }
   float h[4] = {0.f, 0.f, 0.f, 0.f};
@@ -432,13 +490,23 @@ __global__ void __launch_bounds__(256, 2) scan_bwd(ScanParams p) {
   for (int i = 0; i < L; ++i) any |= info[chunk * L + i];
   const bool plain = !__any((any & 3) != 0);
 
-  float side[L][4], u[L][4];
+  float a[L][4], keep[L][4], u[L][4];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     float g[4];
     F::unpack(gv[i], g);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) side[i][v] = gate_side<T>(g[v]);
+    for (int v = 0; v < 4; ++v) sides<T>(g[v], a[i][v], keep[i][v]);
+  }
+  // rows of no sample become rows of zeros, which begin and hand on nothing
+  if (!plain) {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (info[chunk * L + i] == kNone) {
+        xv[i] = uv[i] = F::none();
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a[i][v] = keep[i][v] = 0.f;
+      }
   }
   // the value that a sample's first row (its last one, in the other direction) begins with
   auto begin = [&](const float* from, int what, float (&f)[4]) {
@@ -450,32 +518,39 @@ __global__ void __launch_bounds__(256, 2) scan_bwd(ScanParams p) {
   float Ab[4] = {1.f, 1.f, 1.f, 1.f}, Bb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = L - 1; i >= 0; --i) {
-    const int what = plain ? 0 : info[chunk * L + i];
-    const bool cut = !plain && (what == kNone || (what & kLast));
     float dy[4];
     F::unpack(uv[i], dy);
-    if (cut) begin(p.dlast, what, Bb);
+    if (!plain) {
+      const int what = info[chunk * L + i];
+      if (what & kLast) {  // kNone has all bits
+        begin(p.dlast, what, Bb);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) Ab[v] = 0.f;
+      }
+    }
+    // a NaN decay makes A one where it should stay 0, but B as well
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float a = decay_of(side[i][v]);
-      Bb[v] = !plain && what == kNone ? 0.f : a * (dy[v] + Bb[v]);
-      Ab[v] = cut ? 0.f : times(Ab[v], a);
+      Bb[v] = a[i][v] * (dy[v] + Bb[v]);
+      Ab[v] *= a[i][v];
     }
   }
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const int what = plain ? 0 : info[chunk * L + i];
-    const bool cut = !plain && (what == kNone || (what & kFirst));
     float x[4];
     F::unpack(xv[i], x);
+    if (!plain) {
+      const int what = info[chunk * L + i];
+      if (what & kFirst) {
+        begin(p.h0, what, B);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
-    if (cut) begin(p.h0, what, B);
+        for (int v = 0; v < 4; ++v) A[v] = 0.f;
+      }
+    }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float a = decay_of(side[i][v]);
-      B[v] = !plain && what == kNone ? 0.f : fmaf(a, B[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
-      A[v] = cut ? 0.f : times(A[v], a);
+      B[v] = fmaf(a[i][v], B[v], MIX ? keep[i][v] * x[v] : x[v]);
+      A[v] *= a[i][v];
     }
   }
   TL::template join<true>(Ab, Bb, totb);
@@ -486,43 +561,48 @@ __global__ void __launch_bounds__(256, 2) scan_bwd(ScanParams p) {
   if (p.tiles > 1) look_back<CL, true>(p, order, group, totb, link, c);
   TL::template enter<false>(h, A, B, tot);
   TL::template enter<true>(c, Ab, Bb, totb);
+  if (!mine) return;
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const int what = plain ? 0 : info[chunk * L + i];
     float x[4];
     afresh(xv[i]);
     F::unpack(xv[i], x);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
-    if (!plain && (what == kNone || (what & kFirst))) begin(p.h0, what, h);
+    if (!plain) {
+      const int what = info[chunk * L + i];
+      if (what & kFirst) begin(p.h0, what, h);
+    }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       u[i][v] = MIX ? h[v] - x[v] : h[v];
-      h[v] = !plain && what == kNone ? 0.f : fmaf(decay_of(side[i][v]), h[v], MIX ? keep_of(side[i][v]) * x[v] : x[v]);
+      h[v] = fmaf(a[i][v], h[v], MIX ? keep[i][v] * x[v] : x[v]);
     }
   }
+  Lane dxl, dgl;
+  dxl.init(p.dx, p.c * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
+  dgl.init(p.dgate, p.c * int64_t(sizeof(T)), p, first, chunk * L, kRows, col);
 #pragma unroll
   for (int i = L - 1; i >= 0; --i) {
-    const int what = plain ? 0 : info[chunk * L + i];
-    const bool none = !plain && what == kNone;
     float dy[4], dx[4], dg[4];
     afresh(uv[i]);
     F::unpack(uv[i], dy);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) afresh(side[i][v]);
-    if (!plain && (none || (what & kLast))) begin(p.dlast, what, c);
+    if (!plain) {
+      const int what = info[chunk * L + i];
+      if (what & kLast) begin(p.dlast, what, c);
+    }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float q = fabsf(side[i][v]), d = dy[v] + c[v];
-      dx[v] = none ? 0.f : (MIX ? keep_of(side[i][v]) * d : d);
-      dg[v] = none ? 0.f : q * (1.f - q) * d * u[i][v];
-      c[v] = none ? 0.f : decay_of(side[i][v]) * d;
+      const float d = dy[v] + c[v], kd = keep[i][v] * d;
+      dx[v] = MIX ? kd : d;
+      dg[v] = kd * u[i][v] * a[i][v];
+      c[v] = a[i][v] * d;
     }
-    if (i >= rows) continue;
-    const int64_t at = (row0 + i * step) * p.c + c0;
-    *reinterpret_cast<typename F::raw*>(static_cast<T*>(p.dx) + at) = F::pack(dx);
-    *reinterpret_cast<typename F::raw*>(static_cast<T*>(p.dgate) + at) = F::pack(dg);
-    if (!plain && !none && (what & kFirst) && p.dh0) store_state(p.dh0 + int64_t(what >> 2) * p.c + c0, c);
+    if (!whole && i >= rows) continue;
+    dxl.put(i, F::pack(dx));
+    dgl.put(i, F::pack(dg));
+    if (!plain && p.dh0) {
+      const int what = info[chunk * L + i];
+      if (what != kNone && (what & kFirst)) store_state(p.dh0 + int64_t(what >> 2) * p.c + c0, c);
+    }
   }
 }
 
@@ -538,23 +618,28 @@ __global__ void __launch_bounds__(256) scan_clear(uint4* maps, int64_t nmaps, ui
 int esize(int32_t dtype) { return dtype == SSC_F32 ? 4 : 2; }
 bool bad(const void* ptr) { return !ptr || !aligned16(ptr); }
 
-// Rows of a thread, lanes of a tile's row, tiles along the rows and groups of channels
+// Rows of a thread, lanes of a tile's row, tiles along the rows of either pass and groups of channels
 struct ScanPlan {
-  int rows, lanes;
-  int64_t tiles, groups;
+  bool few;  // see kFewTiles
+  int lanes;
+  int64_t fwd_tiles, bwd_tiles, groups;
 };
+constexpr int kFewRows = 4, kBackRows = 8;
+constexpr int fwd_rows(int esize) { return esize == 2 ? 16 : 8; }
+constexpr int64_t kFewTiles = 512;
+
+int64_t scan_tiles(int64_t n, int lanes, int rows) {
+  const int64_t per = int64_t(256 / lanes) * rows;
+  return n > 0 ? (n + per - 1) / per : 1;
+}
 ScanPlan scan_plan(const ssc_scan_shape& a) {
   const int vecs = a.channels / kFour;
   ScanPlan s{};
   s.lanes = vecs <= 8 ? 8 : 16;
-  s.rows = a.dtype == SSC_F32 ? 8 : 16;
   s.groups = (vecs + s.lanes - 1) / s.lanes;
-  auto tiles = [&]() {
-    const int64_t rows = int64_t(256 / s.lanes) * s.rows;
-    return a.n > 0 ? (a.n + rows - 1) / rows : 1;
-  };
-  if (tiles() * s.groups < 512) s.rows = 4;
-  s.tiles = tiles();
+  s.few = scan_tiles(a.n, s.lanes, kBackRows) * s.groups < kFewTiles;
+  s.fwd_tiles = scan_tiles(a.n, s.lanes, s.few ? kFewRows : fwd_rows(esize(a.dtype)));
+  s.bwd_tiles = scan_tiles(a.n, s.lanes, s.few ? kFewRows : kBackRows);
   return s;
 }
 
@@ -567,20 +652,20 @@ int scan_check(const ssc_scan_shape* a) {
   if (a->channels > SSC_MAX_SEQ_CHANNELS || a->channels % vec != 0) return SSC_ERR_UNSUPPORTED;
   if (a->form != SSC_SCAN_MIX && a->form != SSC_SCAN_SUM) return SSC_ERR_UNSUPPORTED;
   for (int64_t v : {a->x_row_stride, a->gate_row_stride})
-    if (v < 0 || v > (1LL << 40) || v % vec != 0) return SSC_ERR_INVALID_ARG;
+    if (v < 0 || v > SSC_MAX_SCAN_ROW_STRIDE || v % vec != 0) return SSC_ERR_INVALID_ARG;
   const ScanPlan s = scan_plan(*a);
   // HIP takes fewer than 2^32 threads in a dimension of a launch
-  return s.tiles * s.groups * 256 < (1LL << 32) ? SSC_OK : SSC_ERR_UNSUPPORTED;
+  return s.bwd_tiles * s.groups * 256 < (1LL << 32) ? SSC_OK : SSC_ERR_UNSUPPORTED;
 }
 
-ScanParams scan_params(const ssc_scan_shape& a, const ScanPlan& s) {
+ScanParams scan_params(const ssc_scan_shape& a, const ScanPlan& s, bool back) {
   ScanParams p{};
   p.n = a.n;
   p.x_row = a.x_row_stride;
   p.gate_row = a.gate_row_stride;
   p.c = a.channels;
   p.batch = a.batch;
-  p.tiles = int32_t(s.tiles);
+  p.tiles = int32_t(back ? s.bwd_tiles : s.fwd_tiles);
   p.groups = int32_t(s.groups);
   p.rev = a.reverse != 0;
   return p;
@@ -588,7 +673,7 @@ ScanParams scan_params(const ssc_scan_shape& a, const ScanPlan& s) {
 
 size_t carry_bytes(const ssc_scan_shape& a) {
   const ScanPlan s = scan_plan(a);
-  return size_t(s.tiles) * size_t(a.channels) * 4;
+  return size_t(s.bwd_tiles) * size_t(a.channels) * 4;
 }
 
 struct ScanWs {
@@ -602,36 +687,36 @@ ScanWs scan_ws(const ssc_scan_shape& a) {
   return w;
 }
 
-template <typename T, int CL, int L>
+template <typename T, int CL, int L, int LB>
 void scan_launch(const ScanParams& p, bool mix, bool back, hipStream_t s) {
   const unsigned grid = unsigned(int64_t(p.tiles) * p.groups);
   if (back) {
     if (mix)
-      scan_bwd<T, CL, L, true><<<grid, 256, 0, s>>>(p);
+      scan_bwd<T, CL, LB, true><<<grid, 256, 0, s>>>(p);
     else
-      scan_bwd<T, CL, L, false><<<grid, 256, 0, s>>>(p);
+      scan_bwd<T, CL, LB, false><<<grid, 256, 0, s>>>(p);
   } else {
     if (mix)
-      scan_fwd<T, CL, L, true><<<grid, 256, 0, s>>>(p);
+      scan_fwd<T, CL, L, LB, true><<<grid, 256, 0, s>>>(p);
     else
-      scan_fwd<T, CL, L, false><<<grid, 256, 0, s>>>(p);
+      scan_fwd<T, CL, L, LB, false><<<grid, 256, 0, s>>>(p);
   }
+}
+
+template <typename T, int CL>
+void scan_rows(const ScanPlan& f, const ScanParams& p, bool mix, bool back, hipStream_t s) {
+  if (f.few)
+    scan_launch<T, CL, kFewRows, kFewRows>(p, mix, back, s);
+  else
+    scan_launch<T, CL, fwd_rows(sizeof(T)), kBackRows>(p, mix, back, s);
 }
 
 template <typename T>
 void scan_form(const ScanPlan& f, const ScanParams& p, bool mix, bool back, hipStream_t s) {
-  constexpr int kRows = sizeof(T) == 4 ? 8 : 16;
-  if (f.lanes == 8) {
-    if (f.rows == 4)
-      scan_launch<T, 8, 4>(p, mix, back, s);
-    else
-      scan_launch<T, 8, kRows>(p, mix, back, s);
-  } else {
-    if (f.rows == 4)
-      scan_launch<T, 16, 4>(p, mix, back, s);
-    else
-      scan_launch<T, 16, kRows>(p, mix, back, s);
-  }
+  if (f.lanes == 8)
+    scan_rows<T, 8>(f, p, mix, back, s);
+  else
+    scan_rows<T, 16>(f, p, mix, back, s);
 }
 
 int scan_run(const ssc_scan_shape& a, const ScanPlan& sp, const ScanParams& p, bool back, void* stream) {
@@ -677,7 +762,7 @@ extern "C" int ssc_gated_scan_fwd(const ssc_scan_shape* shape, const void* x, co
   const ScanWs w = scan_ws(a);
   if (workspace_bytes < w.total) return SSC_ERR_WORKSPACE;
   const ScanPlan sp = scan_plan(a);
-  ScanParams p = scan_params(a, sp);
+  ScanParams p = scan_params(a, sp, false);
   char* ws = static_cast<char*>(workspace);
   p.x = x;
   p.gate = gate;
@@ -687,7 +772,8 @@ extern "C" int ssc_gated_scan_fwd(const ssc_scan_shape* shape, const void* x, co
   p.last = last;
   p.ticket = reinterpret_cast<uint32_t*>(ws);
   p.maps = reinterpret_cast<uint64_t*>(ws + w.maps);
-  p.values = carries ? reinterpret_cast<uint32_t*>(carries) : reinterpret_cast<uint32_t*>(ws + w.values);
+  p.values = reinterpret_cast<uint32_t*>(ws + w.values);
+  p.carries = carries;
   return scan_run(a, sp, p, false, stream);
 }
 
@@ -703,7 +789,7 @@ extern "C" int ssc_gated_scan_bwd(const ssc_scan_shape* shape, const void* x, co
   const ScanWs w = scan_ws(a);
   if (workspace_bytes < w.total) return SSC_ERR_WORKSPACE;
   const ScanPlan sp = scan_plan(a);
-  ScanParams p = scan_params(a, sp);
+  ScanParams p = scan_params(a, sp, true);
   char* ws = static_cast<char*>(workspace);
   p.x = x;
   p.gate = gate;
@@ -717,6 +803,6 @@ extern "C" int ssc_gated_scan_bwd(const ssc_scan_shape* shape, const void* x, co
   p.ticket = reinterpret_cast<uint32_t*>(ws);
   p.maps = reinterpret_cast<uint64_t*>(ws + w.maps);
   p.values = reinterpret_cast<uint32_t*>(ws + w.values);
-  p.carries = carries;
+  p.carries = const_cast<float*>(carries);
   return scan_run(a, sp, p, true, stream);
 }
