@@ -10,7 +10,7 @@
 // Both directions compose maps v -> A v + B, which is associative.  A thread walks L rows of four channels, CL lanes beside
 // it the neighbouring channels, and the 256 / CL threads along the rows are joined by shuffles and LDS: a tile of
 // 256 L / CL rows by 4 CL channels, read once.  Tiles are joined as they run: each publishes its map, takes the value
-// behind the tile kReach before it and the maps of those between, and publishes the value behind itself.  Which words a
+// behind the tile REACH before it and the maps of those between, and publishes the value behind itself.  Which words a
 // tile takes is fixed, so sums have one order and results repeat.  Tiles take their numbers from a counter in the order
 // they start: a tile only waits for tiles that run already and that never wait for it.  A published word is its own flag:
 // it was cleared to all ones, a NaN that no result is given, and is written once, so no order between words matters.
@@ -29,8 +29,12 @@ namespace ssc {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kReach = 16;   // tiles that a tile looks back over
-constexpr int kFour = 4;     // channels of a thread
+constexpr int kFour = 4;  // channels of a thread
+constexpr int kFewRows = 4, kBackRows = 8;
+constexpr int fwd_rows(int esize) { return esize == 2 ? 16 : 8; }
+// Tiles that a tile looks back over: what is known moves so many tiles on with each exchange between tiles, of about a
+// microsecond.
+constexpr int reach(int rows) { return rows == kFewRows ? 64 : 16; }
 
 struct ScanParams {
   const void *x, *gate, *dy;
@@ -249,13 +253,13 @@ __device__ __forceinline__ uint32_t word_of(float f) {
   return u == kNotYet ? 0x7FC00000u : u;
 }
 
-// The value that reaches tile `order` (of the order of work): per channel, a lane of each wave composes four of the maps
-// of tiles order - kReach .. order - 1 (the first one the value behind its tile), LDS joins the waves, and the first
+// The value that reaches tile `order` (of the order of work): per channel, a lane of each wave composes a quarter of the maps
+// of tiles order - REACH .. order - 1 (the first one the value behind its tile), LDS joins the waves, and the first
 // wave publishes the value behind this tile.  `link` [4][2][4 CL].  Returns the thread's own channels' value in v.
-template <int CL, bool BACK>
+template <int CL, int REACH, bool BACK>
 __device__ __forceinline__ void look_back(const ScanParams& p, int order, int group, const float (*tot)[2][4 * CL],
                                           float (*link)[2][4 * CL], float (&v)[4]) {
-  constexpr int CH = 4 * CL, K = kReach / 4;
+  constexpr int CH = 4 * CL, K = REACH / 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = group * CH + lane;
   const bool here = lane < CH && ch < p.c;
   float mA = 1.f, mB = 0.f;
@@ -266,7 +270,7 @@ __device__ __forceinline__ void look_back(const ScanParams& p, int order, int gr
   }
   float A = 1.f, B = 0.f;
   if (here) {
-    const int first = order - kReach + wave * K;
+    const int first = order - REACH + wave * K;
     uint64_t w[K];
     bool done;
     do {
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_fwd(ScanPara
   __syncthreads();
   empty_samples<CL>(p, tile, c0, mine, p.h0, p.last);
   float h[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.tiles > 1) look_back<CL, false>(p, tile, group, tot, link, h);
+  if (p.tiles > 1) look_back<CL, reach(L), false>(p, tile, group, tot, link, h);
   TL::template enter<false>(h, A, B, tot);
   if (!mine) return;
   constexpr int kParts = L / LB, kPart = 256 / CL / kParts;
@@ -558,7 +562,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanPara
   __syncthreads();
   empty_samples<CL>(p, tile, c0, mine, p.dlast, p.dh0);
   float c[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.tiles > 1) look_back<CL, true>(p, order, group, totb, link, c);
+  if (p.tiles > 1) look_back<CL, reach(L), true>(p, order, group, totb, link, c);
   TL::template enter<false>(h, A, B, tot);
   TL::template enter<true>(c, Ab, Bb, totb);
   if (!mine) return;
@@ -624,8 +628,6 @@ struct ScanPlan {
   int lanes;
   int64_t fwd_tiles, bwd_tiles, groups;
 };
-constexpr int kFewRows = 4, kBackRows = 8;
-constexpr int fwd_rows(int esize) { return esize == 2 ? 16 : 8; }
 constexpr int64_t kFewTiles = 512;
 
 int64_t scan_tiles(int64_t n, int lanes, int rows) {
