@@ -65,10 +65,15 @@ template <int N>
 __device__ __forceinline__ void drop(float (&f)[N], int64_t e0, const Drop& d, const DropKey& key) {
   uint32_t w[4];
   philox(uint32_t(uint64_t(e0) >> 3), d.layer, key, w);
-  const bool upper = N == 4 && (e0 & 4);
+  // four elements take two of the words: chosen bit by bit, as a choice of addresses would put the words into memory
+  if constexpr (N == 4) {
+    const uint32_t upper = e0 & 4 ? ~0u : 0u;
+    w[0] ^= (w[0] ^ w[2]) & upper;
+    w[1] ^= (w[1] ^ w[3]) & upper;
+  }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const uint32_t word = N == 8 ? w[j / 2] : (upper ? w[2 + j / 2] : w[j / 2]);
+    const uint32_t word = w[j / 2];
     const uint32_t bits = (j & 1) ? word >> 16 : word & 0xFFFFu;
     f[j] = bits >= d.t ? f[j] * d.scale : 0.f;
   }

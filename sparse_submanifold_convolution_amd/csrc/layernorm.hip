@@ -78,7 +78,7 @@ __device__ __forceinline__ float centre(float (&f)[V][N], const bool (&mine)[V],
 }
 
 template <typename T, int L, int V, bool RES, bool DROP>
-__global__ void __launch_bounds__(256) norm_fwd(NormParams p) {
+__global__ void __launch_bounds__(256, 4) norm_fwd(NormParams p) {
   constexpr int N = Vec<T>::N;
   __shared__ float lds[L > 64 ? 2 : 1][4][2];
   int turn = 0;
@@ -133,10 +133,17 @@ __global__ void __launch_bounds__(256) norm_fwd(NormParams p) {
   }
 }
 
+// Waves per SIMD that the backward kernel's registers are held to, by the elements of a lane.  Its grid is what then fits
+// the chip at once: with 2,048 workgroups in two and two thirds rounds a tenth of the time went to the last one.
+constexpr int bwd_waves(int esize, int vecs) {
+  const int elements = vecs * 16 / esize;
+  return elements <= 8 ? 4 : (elements <= 16 ? 3 : (esize == 2 ? 2 : 1));
+}
+
 // Rows are taken in turn by the grid's groups; dw and db of the group's channels stay in registers (DW) and are added
 // over the workgroup's groups at the end.
 template <typename T, int L, int V, bool RES, bool DROP, bool DW>
-__global__ void __launch_bounds__(256) norm_bwd(NormParams p) {
+__global__ void __launch_bounds__(256, bwd_waves(sizeof(T), V)) norm_bwd(NormParams p) {
   constexpr int N = Vec<T>::N, GPB = 256 / L;
   __shared__ float lds[L > 64 ? 2 : 1][4][2];
   int turn = 0;
@@ -145,20 +152,20 @@ __global__ void __launch_bounds__(256) norm_bwd(NormParams p) {
   DropKey key;
   if constexpr (DROP) key.load(p.drop.rng);
   bool mine[V];
-  float w[V][N], dw[DW ? V : 1][N], db[DW ? V : 1][N];
+  u32x4 wv[V];
+  float dw[DW ? V : 1][N], db[DW ? V : 1][N];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = (sub + i * L) * N;
     mine[i] = e < p.c;
-#pragma unroll
-    for (int j = 0; j < N; ++j) w[i][j] = 1.f;
-    if (p.w && mine[i]) Vec<T>::unpack(*reinterpret_cast<const u32x4*>(static_cast<const T*>(p.w) + e), w[i]);
+    wv[i] = u32x4{0, 0, 0, 0};
+    if (p.w && mine[i]) wv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.w) + e);
     if constexpr (DW)
 #pragma unroll
       for (int j = 0; j < N; ++j) dw[i][j] = db[i][j] = 0.f;
   }
-  for (int64_t row = int64_t(blockIdx.x) * GPB + grp; row < p.n; row += int64_t(gridDim.x) * GPB) {
-    u32x4 xv[V], gv[V], uv[RES ? V : 1];
+  u32x4 xv[V], gv[V], uv[RES ? V : 1];
+  auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = (sub + i * L) * N;
@@ -171,14 +178,23 @@ __global__ void __launch_bounds__(256) norm_bwd(NormParams p) {
           if (p.ds) uv[i] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.ds) + row * p.c + e);
       }
     }
-    float f[V][N];
-#pragma unroll
-    for (int i = 0; i < V; ++i) Vec<T>::unpack(xv[i], f[i]);
-    const float r = centre<L>(f, mine, inv_c, p.eps, lds, turn);
-    float g[V][N], sums[2] = {0.f, 0.f};
+  };
+  const int64_t step = int64_t(gridDim.x) * GPB;
+  for (int64_t row = int64_t(blockIdx.x) * GPB + grp; row < p.n; row += step) {
+    load(row);
+    float f[V][N], g[V][N], u[RES ? V : 1][N];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      Vec<T>::unpack(xv[i], f[i]);
       Vec<T>::unpack(gv[i], g[i]);
+      if constexpr (RES) Vec<T>::unpack(uv[i], u[i]);
+    }
+    const float r = centre<L>(f, mine, inv_c, p.eps, lds, turn);
+    float sums[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float w[N];
+      Vec<T>::unpack(wv[i], w);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         f[i][j] *= r;
@@ -186,7 +202,7 @@ __global__ void __launch_bounds__(256) norm_bwd(NormParams p) {
           dw[i][j] = fmaf(g[i][j], f[i][j], dw[i][j]);
           db[i][j] += g[i][j];
         }
-        g[i][j] *= w[i][j];
+        if (p.w) g[i][j] *= w[j];
         sums[0] += g[i][j];
         sums[1] = fmaf(g[i][j], f[i][j], sums[1]);
       }
@@ -200,10 +216,8 @@ __global__ void __launch_bounds__(256) norm_bwd(NormParams p) {
 #pragma unroll
       for (int j = 0; j < N; ++j) g[i][j] = r * (g[i][j] - mg - f[i][j] * mz);
       if constexpr (RES) {
-        float u[N];
-        Vec<T>::unpack(uv[i], u);
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[i][j] += u[j];
+        for (int j = 0; j < N; ++j) g[i][j] += u[i][j];
         if (p.dres) *reinterpret_cast<u32x4*>(static_cast<T*>(p.dres) + at) = Vec<T>::pack(g[i]);
       }
       if (p.dx) {
@@ -354,10 +368,11 @@ RowForm row_form(int64_t channels, int32_t dtype) {
   return {256, 8};
 }
 
-// Workgroups of the backward grid: enough to fill the chip, no more than the rows need
+// Workgroups of the backward grid: as many as fit the chip's 256 CUs at once, no more than the rows need
 int64_t row_blocks(const ssc_layer_norm_shape& a) {
-  const int gpb = 256 / row_form(a.channels, a.dtype).lanes;
-  const int64_t need = (a.n + gpb - 1) / gpb, most = 2048;
+  const RowForm f = row_form(a.channels, a.dtype);
+  const int gpb = 256 / f.lanes;
+  const int64_t need = (a.n + gpb - 1) / gpb, most = 256 * bwd_waves(esize(a.dtype), f.vecs);
   return need < 1 ? 1 : (need < most ? need : most);
 }
 

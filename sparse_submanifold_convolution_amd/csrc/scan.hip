@@ -9,11 +9,15 @@
 //
 // Both directions compose maps v -> A v + B, which is associative.  A thread walks L rows of four channels, CL lanes beside
 // it the neighbouring channels, and the 256 / CL threads along the rows are joined by shuffles and LDS: a tile of
-// 256 L / CL rows by 4 CL channels, read once.  Tiles are joined as they run: each publishes its map, takes the value
-// behind the tile REACH before it and the maps of those between, and publishes the value behind itself.  Which words a
-// tile takes is fixed, so sums have one order and results repeat.  Tiles take their numbers from a counter in the order
-// they start: a tile only waits for tiles that run already and that never wait for it.  A published word is its own flag:
-// it was cleared to all ones, a NaN that no result is given, and is written once, so no order between words matters.
+// 256 L / CL rows by 4 CL channels, read once.  Tiles are joined as they run: each publishes its map and takes what
+// others have published (see look_back).  Which words a tile takes is fixed, so sums have one order and results repeat.
+// Tiles take their numbers from a counter in the order they start: a tile only waits for tiles that run already and that
+// never wait for it.  A published word is its own flag: it was cleared to all ones, a NaN that no result is given, and is
+// written once, so no order between words matters.
+//
+// Bound by memory where rows are wide: 629k rows x 1,024 channels, bf16, forward 0.76 ms (5.1 TB/s), backward 1.39 ms
+// (4.6 TB/s); narrow ones by the exchange between tiles (800k rows x 64 channels: 0.11 and 0.18 ms, 2.8 TB/s).  In three
+// launches, with the inputs read twice and the tiles joined in between, the forward pass would move 5 tensors, not 3.
 //
 // A sample's first row has A = 0, and A = 0 drops whatever came before it, so samples never touch each other, not even
 // through an infinity or a NaN.  States, products and sums are fp32.  The backward pass forms h again from the inputs and
@@ -30,11 +34,16 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFour = 4;  // channels of a thread
-constexpr int kFewRows = 4, kBackRows = 8;
-constexpr int fwd_rows(int esize) { return esize == 2 ? 16 : 8; }
-// Tiles that a tile looks back over: what is known moves so many tiles on with each exchange between tiles, of about a
-// microsecond.
-constexpr int reach(int rows) { return rows == kFewRows ? 64 : 16; }
+// Tiles of a bunch, and bunches that a tile looks back over: what is known moves on by 56 tiles with each exchange between
+// tiles, of about 2 us, and a tile takes 3.5 + 8 words on average.  A plain row of 16 tiles (16 words) left narrow rows
+// waiting (800k rows x 64 channels, bf16: forward 196 us, now 108; x 256: 301 and 299), three bunches did as well (142 us),
+// and bunches of 16 take more words and registers than they save (x 256 backward: 524 -> 798 us).
+constexpr int kBunch = 8, kBunches = 7;
+// Rows of a thread.  Forward, 16 bits: 16 keep 128 registers of decays and inputs, at three waves per SIMD; 8 leave room for
+// four, but tiles half as long (800k rows x 256 channels: 341 us, with 16 rows 299).  The backward pass keeps three values
+// an element and fp32 twice the raw rows.  With few tiles shorter ones spread the work.
+constexpr int kBackRows = 8;
+constexpr int fwd_rows(int esize, bool few) { return esize == 2 && !few ? 16 : 8; }
 
 struct ScanParams {
   const void *x, *gate, *dy;
@@ -44,8 +53,9 @@ struct ScanParams {
   float *last, *dh0;
   float* carries;        // h before the first row of each tile of the backward pass
   uint32_t* ticket;
-  uint64_t* maps;        // [tiles][C], by the order of work: a tile's map, A in the low word
-  uint32_t* values;      // [tiles][C], by the order of work: the value that reaches the tile
+  // words between tiles, by the order of work, A in the low half: the tiles' maps [tiles][C], the maps of bunches of tiles
+  // and the values that reach them [bunches][C]
+  uint64_t *maps, *bunches, *values;
   int64_t n, x_row, gate_row;
   int32_t c, batch, tiles, groups, rev;
 };
@@ -253,64 +263,73 @@ __device__ __forceinline__ uint32_t word_of(float f) {
   return u == kNotYet ? 0x7FC00000u : u;
 }
 
-// The value that reaches tile `order` (of the order of work): per channel, a lane of each wave composes a quarter of the maps
-// of tiles order - REACH .. order - 1 (the first one the value behind its tile), LDS joins the waves, and the first
-// wave publishes the value behind this tile.  `link` [4][2][4 CL].  Returns the thread's own channels' value in v.
-template <int CL, int REACH, bool BACK>
-__device__ __forceinline__ void look_back(const ScanParams& p, int order, int group, const float (*tot)[2][4 * CL],
-                                          float (*link)[2][4 * CL], float (&v)[4]) {
-  constexpr int CH = 4 * CL, K = REACH / 4;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = group * CH + lane;
-  const bool here = lane < CH && ch < p.c;
-  float mA = 1.f, mB = 0.f;
-  if (wave == 0 && here) {
-    Tile<CL>::template whole<BACK>(tot, lane, &mA, &mB);
-    __hip_atomic_store(p.maps + int64_t(order) * p.c + ch, uint64_t(__float_as_uint(mB)) << 32 | word_of(mA), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  }
-  float A = 1.f, B = 0.f;
-  if (here) {
-    const int first = order - REACH + wave * K;
-    uint64_t w[K];
-    bool done;
-    do {
-      done = true;
+// Waits for n of K words `step` apart, of which the first lies at `head` and the k-th at at + k step, and composes their
+// maps in order.
+template <int K>
+__device__ __forceinline__ void take_words(const uint64_t* head, const uint64_t* at, int64_t step, int n, float& A, float& B) {
+  uint64_t w[K];
+  bool done;
+  do {
+    done = true;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int t = first + k;
-        if (t < 0)
-          w[k] = uint64_t(__float_as_uint(1.f));  // no tile: the value stays
-        else if (wave == 0 && k == 0)
-          w[k] = uint64_t(__hip_atomic_load(p.values + int64_t(t + 1) * p.c + ch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) << 32;
-        else
-          w[k] = __hip_atomic_load(p.maps + int64_t(t) * p.c + ch, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+    for (int k = 0; k < K; ++k)
+      if (k < n) w[k] = __hip_atomic_load(k == 0 ? head : at + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        done &= (wave == 0 && k == 0 && first >= 0 ? uint32_t(w[k] >> 32) : uint32_t(w[k])) != kNotYet;
-      if (!done) __builtin_amdgcn_s_sleep(1);
-    } while (!done);
+    for (int k = 0; k < K; ++k)
+      if (k < n) done &= uint32_t(w[k]) != kNotYet;
+    if (!done) __builtin_amdgcn_s_sleep(1);
+  } while (!done);
+  A = 1.f;
+  B = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k)
+    if (k < n) {
       const float a = __uint_as_float(uint32_t(w[k])), b = __uint_as_float(uint32_t(w[k] >> 32));
       B = after(a, b, B);
       A = times(a, A);
+    }
+}
+__device__ __forceinline__ void give_word(uint64_t* at, float A, float B) {
+  __hip_atomic_store(at, uint64_t(__float_as_uint(B)) << 32 | word_of(A), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The value that reaches tile `order` (of the order of work), for the thread's own channels.  Tiles come in bunches of
+// kBunch.  Per channel, a lane of the first wave publishes the tile's map and composes those of the bunch's tiles before
+// it, and the last tile's publishes the bunch's; a lane of the second wave composes the maps of the kBunches bunches
+// before this one upon the value that reached the first of them, and the first tile's publishes the value that reaches the
+// bunch.  A value is a word with A = 0.
+template <int CL, bool BACK>
+__device__ __forceinline__ void look_back(const ScanParams& p, int order, int group, const float (*tot)[2][4 * CL],
+                                          float (*link)[2][4 * CL], float (&v)[4]) {
+  constexpr int CH = 4 * CL;
+  const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), ch = group * CH + lane;
+  const int bunch = order / kBunch, place = order % kBunch;
+  const bool here = lane < CH && ch < p.c;
+  if (wave < 2 && here) {
+    float A, B;
+    if (wave == 0) {
+      float mA, mB;
+      Tile<CL>::template whole<BACK>(tot, lane, &mA, &mB);
+      uint64_t* mine = p.maps + int64_t(order) * p.c + ch;
+      give_word(mine, mA, mB);
+      const uint64_t* from = mine - int64_t(place) * p.c;
+      take_words<kBunch - 1>(from, from, p.c, place, A, B);
+      if (place == kBunch - 1) give_word(p.bunches + int64_t(bunch) * p.c + ch, times(mA, A), after(mA, mB, B));
+    } else {
+      // the value that reached bunch `from`, then that bunch and those after it
+      const int from = bunch > kBunches ? bunch - kBunches : 0;
+      take_words<kBunches + 1>(p.values + int64_t(from) * p.c + ch, p.bunches + (int64_t(from) - 1) * p.c + ch, p.c,
+                               bunch - from + 1, A, B);
+      if (place == 0 && bunch > 0) give_word(p.values + int64_t(bunch) * p.c + ch, A, B);
     }
     link[wave][0][lane] = A;
     link[wave][1][lane] = B;
   }
   __syncthreads();
-  if (wave == 0 && here && order + 1 < p.tiles) {
-    float f = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) f = after(link[w][0][lane], link[w][1][lane], f);
-    __hip_atomic_store(p.values + int64_t(order + 1) * p.c + ch, word_of(after(mA, mB, f)), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  }
   const int col = threadIdx.x % CL;
   if (group * CH + col * 4 < p.c)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 1; w >= 0; --w) {
       float a[4], b[4];
       load_state(&link[w][0][col * 4], a);
       load_state(&link[w][1][col * 4], b);
@@ -350,7 +369,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_fwd(ScanPara
   using F = Four<T>;
   constexpr int kRows = 256 / CL * L;
   __shared__ __align__(16) int info[kRows];
-  __shared__ __align__(16) float tot[4][2][4 * CL], link[4][2][4 * CL];
+  __shared__ __align__(16) float tot[4][2][4 * CL], link[2][2][4 * CL];
+  __shared__ __align__(16) float apart[2][256][4];
   __shared__ int slot;
   const int work = take_ticket(p, &slot), group = work % p.groups, tile = work / p.groups;
   const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * 4;
@@ -419,10 +439,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_fwd(ScanPara
     }
   }
   TL::template join<false>(A, B, tot);
+  // the thread's map waits in LDS while registers hold the words between tiles: with 28 bytes of a lane's registers in
+  // scratch instead of 64, three waves a SIMD are worth having (629k rows x 1,024 channels: 816 -> 763 us)
+  store_state(&apart[0][threadIdx.x][0], A);
+  store_state(&apart[1][threadIdx.x][0], B);
   __syncthreads();
   empty_samples<CL>(p, tile, c0, mine, p.h0, p.last);
   float h[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.tiles > 1) look_back<CL, reach(L), false>(p, tile, group, tot, link, h);
+  if (p.tiles > 1) look_back<CL, false>(p, tile, group, tot, link, h);
+  load_state(&apart[0][threadIdx.x][0], A);
+  load_state(&apart[1][threadIdx.x][0], B);
   TL::template enter<false>(h, A, B, tot);
   if (!mine) return;
   constexpr int kParts = L / LB, kPart = 256 / CL / kParts;
@@ -453,7 +479,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanPara
   using F = Four<T>;
   constexpr int kRows = 256 / CL * L;
   __shared__ __align__(16) int info[kRows];
-  __shared__ __align__(16) float tot[4][2][4 * CL], totb[4][2][4 * CL], link[4][2][4 * CL];
+  __shared__ __align__(16) float tot[4][2][4 * CL], totb[4][2][4 * CL], link[2][2][4 * CL];
   __shared__ int slot;
   const int work = take_ticket(p, &slot), group = work % p.groups, order = work / p.groups, tile = p.tiles - 1 - order;
   const int chunk = threadIdx.x / CL, c0 = (group * CL + threadIdx.x % CL) * 4;
@@ -562,7 +588,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanPara
   __syncthreads();
   empty_samples<CL>(p, tile, c0, mine, p.dlast, p.dh0);
   float c[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.tiles > 1) look_back<CL, reach(L), true>(p, order, group, totb, link, c);
+  if (p.tiles > 1) look_back<CL, true>(p, order, group, totb, link, c);
   TL::template enter<false>(h, A, B, tot);
   TL::template enter<true>(c, Ab, Bb, totb);
   if (!mine) return;
@@ -610,23 +636,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanPara
   }
 }
 
-// Clears the words between tiles (counted in 16-byte pieces) and the counter
-__global__ void __launch_bounds__(256) scan_clear(uint4* maps, int64_t nmaps, uint4* values, int64_t nvalues, uint32_t* ticket) {
+// Clears the words between tiles (in 16-byte pieces; first, per: the first bunch's values) and the counter
+__global__ void __launch_bounds__(256) scan_clear(uint4* words, int64_t n, int64_t first, int64_t per, uint32_t* ticket) {
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const uint4 none = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
-  if (i < nmaps) maps[i] = none;
-  if (i < nvalues) values[i] = none;
+  // what reaches the first bunch is zero
+  if (i < n) words[i] = i >= first && i < first + per ? make_uint4(0, 0, 0, 0) : make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
   if (i == 0) *ticket = 0;
 }
 
 int esize(int32_t dtype) { return dtype == SSC_F32 ? 4 : 2; }
 bool bad(const void* ptr) { return !ptr || !aligned16(ptr); }
 
-// Rows of a thread, lanes of a tile's row, tiles along the rows of either pass and groups of channels
+// Forms of a call
 struct ScanPlan {
-  bool few;  // see kFewTiles
-  int lanes;
-  int64_t fwd_tiles, bwd_tiles, groups;
+  bool few;   // see kFewTiles
+  int lanes;  // of a tile's row
+  int64_t fwd_tiles, bwd_tiles, groups;  // tiles along the rows, groups of channels
 };
 constexpr int64_t kFewTiles = 512;
 
@@ -639,9 +664,9 @@ ScanPlan scan_plan(const ssc_scan_shape& a) {
   ScanPlan s{};
   s.lanes = vecs <= 8 ? 8 : 16;
   s.groups = (vecs + s.lanes - 1) / s.lanes;
-  s.few = scan_tiles(a.n, s.lanes, kBackRows) * s.groups < kFewTiles;
-  s.fwd_tiles = scan_tiles(a.n, s.lanes, s.few ? kFewRows : fwd_rows(esize(a.dtype)));
-  s.bwd_tiles = scan_tiles(a.n, s.lanes, s.few ? kFewRows : kBackRows);
+  s.bwd_tiles = scan_tiles(a.n, s.lanes, kBackRows);
+  s.few = s.bwd_tiles * s.groups < kFewTiles;
+  s.fwd_tiles = scan_tiles(a.n, s.lanes, fwd_rows(esize(a.dtype), s.few));
   return s;
 }
 
@@ -678,39 +703,46 @@ size_t carry_bytes(const ssc_scan_shape& a) {
   return size_t(s.bwd_tiles) * size_t(a.channels) * 4;
 }
 
-struct ScanWs {
-  size_t maps = 256, values = 0, total = 0;  // the counter lies first
-};
-ScanWs scan_ws(const ssc_scan_shape& a) {
-  const size_t n = align_up(carry_bytes(a), 256);
-  ScanWs w;
-  w.values = w.maps + 2 * n;
-  w.total = w.values + n;
-  return w;
+// words between the tiles of a pass: their maps, the bunches' and the values that reach the bunches
+int64_t bunch_count(int64_t tiles) { return (tiles + kBunch - 1) / kBunch; }
+int64_t word_count(int64_t tiles, int64_t channels) { return (tiles + 2 * bunch_count(tiles)) * channels; }
+constexpr size_t kTicketBytes = 256;  // the counter lies first
+
+size_t scan_ws(const ssc_scan_shape& a) {
+  const ScanPlan s = scan_plan(a);
+  const int64_t most = s.fwd_tiles > s.bwd_tiles ? s.fwd_tiles : s.bwd_tiles;
+  return kTicketBytes + size_t(word_count(most, a.channels)) * 8;
 }
 
-template <typename T, int CL, int L, int LB>
+void set_words(ScanParams* p, void* workspace) {
+  p->ticket = static_cast<uint32_t*>(workspace);
+  p->maps = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + kTicketBytes);
+  p->bunches = p->maps + int64_t(p->tiles) * p->c;
+  p->values = p->bunches + bunch_count(p->tiles) * p->c;
+}
+
+template <typename T, int CL, int L>
 void scan_launch(const ScanParams& p, bool mix, bool back, hipStream_t s) {
   const unsigned grid = unsigned(int64_t(p.tiles) * p.groups);
   if (back) {
     if (mix)
-      scan_bwd<T, CL, LB, true><<<grid, 256, 0, s>>>(p);
+      scan_bwd<T, CL, kBackRows, true><<<grid, 256, 0, s>>>(p);
     else
-      scan_bwd<T, CL, LB, false><<<grid, 256, 0, s>>>(p);
+      scan_bwd<T, CL, kBackRows, false><<<grid, 256, 0, s>>>(p);
   } else {
     if (mix)
-      scan_fwd<T, CL, L, LB, true><<<grid, 256, 0, s>>>(p);
+      scan_fwd<T, CL, L, kBackRows, true><<<grid, 256, 0, s>>>(p);
     else
-      scan_fwd<T, CL, L, LB, false><<<grid, 256, 0, s>>>(p);
+      scan_fwd<T, CL, L, kBackRows, false><<<grid, 256, 0, s>>>(p);
   }
 }
 
 template <typename T, int CL>
 void scan_rows(const ScanPlan& f, const ScanParams& p, bool mix, bool back, hipStream_t s) {
   if (f.few)
-    scan_launch<T, CL, kFewRows, kFewRows>(p, mix, back, s);
+    scan_launch<T, CL, fwd_rows(sizeof(T), true)>(p, mix, back, s);
   else
-    scan_launch<T, CL, fwd_rows(sizeof(T)), kBackRows>(p, mix, back, s);
+    scan_launch<T, CL, fwd_rows(sizeof(T), false)>(p, mix, back, s);
 }
 
 template <typename T>
@@ -726,9 +758,9 @@ int scan_run(const ssc_scan_shape& a, const ScanPlan& sp, const ScanParams& p, b
   const bool mix = a.form == SSC_SCAN_MIX;
   (void)hipGetLastError();
   if (p.tiles > 1) {
-    const int64_t words = p.tiles * int64_t(p.c);  // channels come in fours
-    scan_clear<<<unsigned((words / 2 + 255) / 256), 256, 0, s>>>(reinterpret_cast<uint4*>(p.maps), words / 2,
-                                                               reinterpret_cast<uint4*>(p.values), words / 4, p.ticket);
+    const int64_t pieces = word_count(p.tiles, p.c) / 2;  // channels come in fours
+    scan_clear<<<unsigned((pieces + 255) / 256), 256, 0, s>>>(reinterpret_cast<uint4*>(p.maps), pieces,
+                                                           (p.values - p.maps) / 2, p.c / 2, p.ticket);
   }
   if (a.dtype == SSC_F32)
     scan_form<float>(sp, p, mix, back, s);
@@ -750,7 +782,7 @@ extern "C" size_t ssc_gated_scan_carry_bytes(const ssc_scan_shape* shape) {
 }
 
 extern "C" size_t ssc_gated_scan_workspace_bytes(const ssc_scan_shape* shape) {
-  return scan_check(shape) == SSC_OK ? scan_ws(*shape).total : 0;
+  return scan_check(shape) == SSC_OK ? scan_ws(*shape) : 0;
 }
 
 extern "C" int ssc_gated_scan_fwd(const ssc_scan_shape* shape, const void* x, const void* gate, const int32_t* offsets,
@@ -761,20 +793,16 @@ extern "C" int ssc_gated_scan_fwd(const ssc_scan_shape* shape, const void* x, co
   const ssc_scan_shape& a = *shape;
   if (a.n > 0 && (bad(x) || bad(gate) || bad(y))) return SSC_ERR_INVALID_ARG;
   if (bad(offsets) || bad(last) || !aligned16(h0) || !aligned16(carries) || bad(workspace)) return SSC_ERR_INVALID_ARG;
-  const ScanWs w = scan_ws(a);
-  if (workspace_bytes < w.total) return SSC_ERR_WORKSPACE;
+  if (workspace_bytes < scan_ws(a)) return SSC_ERR_WORKSPACE;
   const ScanPlan sp = scan_plan(a);
   ScanParams p = scan_params(a, sp, false);
-  char* ws = static_cast<char*>(workspace);
+  set_words(&p, workspace);
   p.x = x;
   p.gate = gate;
   p.off = offsets;
   p.h0 = h0;
   p.y = y;
   p.last = last;
-  p.ticket = reinterpret_cast<uint32_t*>(ws);
-  p.maps = reinterpret_cast<uint64_t*>(ws + w.maps);
-  p.values = reinterpret_cast<uint32_t*>(ws + w.values);
   p.carries = carries;
   return scan_run(a, sp, p, false, stream);
 }
@@ -788,11 +816,10 @@ extern "C" int ssc_gated_scan_bwd(const ssc_scan_shape* shape, const void* x, co
   if (a.n > 0 && (bad(x) || bad(gate) || bad(dy) || bad(dx) || bad(dgate))) return SSC_ERR_INVALID_ARG;
   if (bad(offsets) || bad(carries) || !aligned16(h0) || !aligned16(dlast) || !aligned16(dh0) || bad(workspace))
     return SSC_ERR_INVALID_ARG;
-  const ScanWs w = scan_ws(a);
-  if (workspace_bytes < w.total) return SSC_ERR_WORKSPACE;
+  if (workspace_bytes < scan_ws(a)) return SSC_ERR_WORKSPACE;
   const ScanPlan sp = scan_plan(a);
   ScanParams p = scan_params(a, sp, true);
-  char* ws = static_cast<char*>(workspace);
+  set_words(&p, workspace);
   p.x = x;
   p.gate = gate;
   p.dy = dy;
@@ -802,9 +829,6 @@ extern "C" int ssc_gated_scan_bwd(const ssc_scan_shape* shape, const void* x, co
   p.dx = dx;
   p.dgate = dgate;
   p.dh0 = dh0;
-  p.ticket = reinterpret_cast<uint32_t*>(ws);
-  p.maps = reinterpret_cast<uint64_t*>(ws + w.maps);
-  p.values = reinterpret_cast<uint32_t*>(ws + w.values);
   p.carries = const_cast<float*>(carries);
   return scan_run(a, sp, p, true, stream);
 }
