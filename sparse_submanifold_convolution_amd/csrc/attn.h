@@ -1281,7 +1281,8 @@ __global__ void __launch_bounds__(NW * 64, SINK ? 1 : tile_cfg(sizeof(T), DP).dk
   if (!find_segment(p.koff, p.nk, p.qoff, p.nq, p.batch, 1, TC, tile, &sg, SINK ? p.sinks : 0x7FFFFFFF)) return;
   const int lane = threadIdx.x & 63, wave = uniform(int(threadIdx.x >> 6)), half = lane >> 5;
   const int dchunks = p.d / TL::kVec;
-  const float c = p.scale * kLog2e;
+  // WIN: a scale of zero clears the keys instead (an unseen score's -inf times 0 would be NaN)
+  const float c = WIN && p.scale == 0.f ? 1.f : p.scale * kLog2e;
   const int dse = DK ? ds_exp<T>(p, hk, sg.index, sg.other, sg.other_len, sg.begin, sg.len) : 0;
   const float dsmul = ldexpf(1.f, dse - kPExp<T>);
 
@@ -1290,7 +1291,7 @@ __global__ void __launch_bounds__(NW * 64, SINK ? 1 : tile_cfg(sizeof(T), DP).dk
   const int64_t row = sg.begin + (live ? col : 0);
   const bool on = live && (!MASK || p.mask[row] != 0);
   u32x4 kf[TL::kFrags], vf[DK ? TL::kFrags : 1];
-  load_cols<T, DP>(static_cast<const T*>(p.k) + row * p.k_row + hk * p.k_head, on, dchunks, kf);
+  load_cols<T, DP>(static_cast<const T*>(p.k) + row * p.k_row + hk * p.k_head, on && !(WIN && p.scale == 0.f), dchunks, kf);
   if constexpr (DK) load_cols<T, DP>(static_cast<const T*>(p.v) + row * p.v_row + hk * p.v_head, on, dchunks, vf);
   f32x16 dk[DK ? TL::kBlocks : 1], dv[DV ? TL::kBlocks : 1];
   auto clear = [&]() {
@@ -1408,6 +1409,21 @@ __global__ void __launch_bounds__(NW * 64, SINK ? 1 : tile_cfg(sizeof(T), DP).dk
         if constexpr (DK) dp[b] = E::mma(TL::rows(td, 32 * b, f), vf[f], dp[b]);
       }
     }
+    if constexpr (WIN)
+      if (part) {
+        // what is not seen gets no weight (c times this is -inf) and no dP, whatever an unseen key's rows hold
+        const float never = c < 0.f ? INFINITY : -INFINITY;
+#pragma unroll
+        for (int b = 0; b < G; ++b) {
+          const uint32_t w = uint32_t(vis >> (32 * b)) >> (4 * half);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const bool on = (w >> (8 * (r / 4) + r % 4)) & 1u;
+            s[b][r] = on ? s[b][r] : never;
+            if constexpr (DK) dp[b][r] = on ? dp[b][r] : 0.f;
+          }
+        }
+      }
 #pragma unroll
     for (int b = 0; b < G; ++b) {
 #pragma unroll
@@ -1418,18 +1434,9 @@ __global__ void __launch_bounds__(NW * 64, SINK ? 1 : tile_cfg(sizeof(T), DP).dk
         const float sh[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, de[4] = {de4.x, de4.y, de4.z, de4.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float pr = __builtin_amdgcn_exp2f(fmaf(s[b][4 * i + j], c, sh[j]));
-          float ds = 0.f;
-          if constexpr (DK) ds = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
-          if constexpr (WIN)
-            if (part) {
-              // both: what a key that is not seen holds does not matter
-              const bool on = (uint32_t(vis >> (32 * b)) >> (8 * i + 4 * half + j)) & 1u;
-              pr = on ? pr : 0.f;
-              ds = on ? ds : 0.f;
-            }
+          const float pr = __builtin_amdgcn_exp2f(fmaf(s[b][4 * i + j], c, sh[j]));
           s[b][4 * i + j] = pr;
-          if constexpr (DK) dp[b][4 * i + j] = ds;
+          if constexpr (DK) dp[b][4 * i + j] = pr * less_delta<T>(dp[b][4 * i + j], de[j], dsmul);
         }
       }
 #pragma unroll
