@@ -272,7 +272,12 @@ def _attn_workspace(sh: bytes, backward: int, dev: torch.device) -> torch.Tensor
     nbytes = int(lib().ssc_cross_attn_workspace_bytes(sh, backward))
     if nbytes == 0:
         raise SSCError("ssc_cross_attn_workspace_bytes", 2)
-    if nbytes == 256 and not backward:  # the smallest size: nothing is kept there
+    return _workspace(nbytes, nbytes == 256 and not backward, dev)  # the smallest size: nothing is kept there
+
+
+def _workspace(nbytes: int, unused: bool, dev: torch.device) -> torch.Tensor:
+    """nbytes of device memory, or 256 that stand for a workspace that is not used."""
+    if unused:
         ws = _unused.get(dev.index)
         if ws is None:
             ws = _unused[dev.index] = torch.empty(256, dtype=torch.uint8, device=dev)

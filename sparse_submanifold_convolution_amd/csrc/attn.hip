@@ -71,8 +71,11 @@ int64_t busy_wgs(int64_t rows, int64_t cols, const ssc_attn_shape& a) {
 // Splits of the forward and dQ passes.  Rows: two workgroups a CU fill the chip; a split is worth its share of the join
 // from four 16-bit tiles on, and from one fp32 tile, whose products take about eight times as long.  Few rows: as
 // many workgroups as fit at once by their LDS, a whole number of times the rows', each wave with two tiles or more.
-int row_split(bool few, int64_t wgs, int64_t kv_tiles, const ssc_attn_shape& a) {
+int row_split(bool few, int64_t wgs, int64_t kv_tiles, const ssc_attn_shape& a, const Window* w) {
   const int e = esize(a.dtype);
+  // a window's few tiles of narrow 16-bit heads are over before a join would be (17 tiles: 13.4 us a call in one split,
+  // 16.0 in two; 33 tiles in a graph: 16.3 and, in four, 11.9)
+  if (few && w && e == 2 && a.head_dim <= 64 && kv_tiles < 24) return 1;
   if (few) return pick_split(wgs, a.head_dim <= 64 ? 2 * kCUs : kCUs, kv_tiles, 8);
   return wgs >= kCUs ? 1 : pick_split(wgs, 2 * kCUs, kv_tiles, e == 4 ? 1 : 4);
 }
@@ -84,7 +87,7 @@ FwdPlan fwd_plan(const ssc_attn_shape& a, const Window* w = nullptr) {
   const int64_t cols = f.few ? 32 : 32 * fwd_waves(esize(a.dtype), a.head_dim > 96 ? 128 : 96);
   const int64_t kv_tiles = ceil_div(seen_rows(w, cols, ceil_div(a.nk, a.batch)), tile_rows(esize(a.dtype)));
   f.tiles = int(rows / cols + a.batch + 2);
-  f.nsplit = row_split(f.few, busy_wgs(rows, cols, a), kv_tiles, a);
+  f.nsplit = row_split(f.few, busy_wgs(rows, cols, a), kv_tiles, a, w);
   return f;
 }
 
@@ -98,17 +101,18 @@ BwdPlan bwd_plan(const ssc_attn_shape& a, const Window* w = nullptr) {
   const int64_t q_tiles = w ? ceil_div(seen_rows(w, kc, tokens) * G, tile_rows(esize(a.dtype))) : q_all;
   b.q_tiles = int(rows / qc + a.batch + 2);
   b.k_tiles = int(a.nk / kc + a.batch + 2);
-  b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a);
+  b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a, w);
   // dK and dV of short encoder sequences: few column tiles over long streams, split into several rounds of workgroups
   // so that the last round's idle CUs and the samples' different lengths matter little (fp32, whose blocks are long:
   // half as many rounds).
   const int64_t wgs = busy_wgs(a.nk, kc, a), want = (a.dtype == SSC_F32 ? 4 : 8) * kCUs;
   b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? 2 : 8);
   if (w && w->sinks > 0) {
-    // the sinks' launch is of single waves over all of a sample's tokens: about eight of them a CU
+    // the sinks' launch is of single waves over all of a sample's tokens: about eight of them a CU, each with one fp32
+    // tile at least (ragged fp32 training, 838 tokens of three heads: 27 us with two)
     const int64_t sinks = w->sinks < a.nk ? w->sinks : a.nk, all = sinks * a.batch < a.nk ? sinks * a.batch : a.nk;
     b.s_tiles = int(all / kSinkCols + a.batch + 2);
-    b.s_split = pick_split(busy_wgs(all, kSinkCols, a), 8 * kCUs, q_all, a.dtype == SSC_F32 ? 2 : 8);
+    b.s_split = pick_split(busy_wgs(all, kSinkCols, a), 8 * kCUs, q_all, a.dtype == SSC_F32 ? 1 : 8);
   }
   return b;
 }

@@ -711,7 +711,7 @@ constexpr size_t kTicketBytes = 256;  // the counter lies first
 size_t scan_ws(const ssc_scan_shape& a) {
   const ScanPlan s = scan_plan(a);
   const int64_t most = s.fwd_tiles > s.bwd_tiles ? s.fwd_tiles : s.bwd_tiles;
-  return kTicketBytes + size_t(word_count(most, a.channels)) * 8;
+  return kTicketBytes + (most > 1 ? size_t(word_count(most, a.channels)) * 8 : 0);  // a single tile exchanges nothing
 }
 
 void set_words(ScanParams* p, void* workspace) {

@@ -10,7 +10,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from .attention import _MAX_ROW_STRIDE, _attn_shape, _dense, _launch, _new, _packed, _ptr
+from .attention import _MAX_ROW_STRIDE, _attn_shape, _dense, _launch, _new, _packed, _ptr, _workspace
 from .binding import DTYPE_CODE, SSCError, _need, lib
 
 # the C structs of the calls' sizes (include/ssc.h), packed: a bytes object is passed as the pointer to them
@@ -283,7 +283,7 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, offsets: torch.Tensor, h
     gated_scan_bwd takes over, where asked for.  One row a sample and h0 make a step of the recurrence."""
     sh, dev, state = _scan_shape(x, gate, offsets, h0, reverse, form)
     nbytes = _scan_bytes("ssc_gated_scan_workspace_bytes", sh)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = _workspace(nbytes, nbytes == 256, dev)  # the smallest size: a single tile exchanges nothing
     y = _new(x)
     last = x.new_empty(state, dtype=torch.float32)
     carries = None
@@ -304,7 +304,7 @@ def gated_scan_bwd(x: torch.Tensor, gate: torch.Tensor, carries: torch.Tensor, d
     if dlast is not None:
         _need(dlast, "dlast", torch.float32, state, dev)
     nbytes = _scan_bytes("ssc_gated_scan_workspace_bytes", sh)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = _workspace(nbytes, nbytes == 256, dev)  # the smallest size: a single tile exchanges nothing
     dx, dgate = torch.empty_like(dy), torch.empty_like(dy)
     dh0 = torch.empty_like(h0) if h0 is not None else None
     _launch("ssc_gated_scan_bwd", dev, sh, _ptr(x), _ptr(gate), _ptr(carries), _ptr(dy), _ptr(offsets), _ptr(h0),
@@ -360,7 +360,7 @@ def _window_workspace(sh: bytes, window: bytes, backward: int, dev: torch.device
     nbytes = int(lib().ssc_window_attn_workspace_bytes(sh, window, backward))
     if nbytes == 0:
         raise SSCError("ssc_window_attn_workspace_bytes", 2)
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return _workspace(nbytes, nbytes == 256 and not backward, dev)  # the smallest size: nothing is kept there
 
 
 def window_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
