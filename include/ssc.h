@@ -560,9 +560,10 @@ int ssc_cross_attn_bwd(const ssc_attn_shape* shape, const void* q, const void* k
  * whose kv_mask byte is not zero: right = 0 is causal, and the first `sinks`
  * keys stay visible to all later rows.  Formulas, sizes, strides, masks, rows
  * of no sample and rounding are those of ssc_cross_attn_*; keys that no row of
- * a sample sees are never used, whatever they hold, but an infinite or NaN key
- * or value row that some row sees may also spoil rows up to a tile (of 256
- * rows at most) away.  The time of a call follows the keys its rows see.
+ * a sample sees are never used, whatever they hold, but an infinite or NaN row
+ * of q, k, v or dout that takes part may also spoil rows of its sample that do
+ * not see it, up to a tile (of 256 rows at most) away.  The time of a call
+ * follows the keys its rows see.
  * ------------------------------------------------------------------------ */
 typedef struct ssc_attn_window {
   int32_t left, right;                   /* keys before and behind a row's own place, at most SSC_MAX_ATTN_ROWS; -1: all */

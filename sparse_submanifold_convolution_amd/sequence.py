@@ -35,12 +35,12 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, 
     return row
 
 
-def _dense_rows(t: torch.Tensor | None) -> torch.Tensor | None:
-    """t itself where the calls take its rows as they lie, else a contiguous copy."""
+def _dense_rows(t: torch.Tensor | None, most: int = 1 << 40) -> torch.Tensor | None:
+    """t itself where the calls take its rows as they lie (at most `most` elements apart), else a contiguous copy."""
     if t is None or t.dim() != 2:
         return t
     taken = (t.stride(1) == 1 or t.shape[1] <= 1) and t.data_ptr() % 16 == 0 and (
-        t.shape[0] <= 1 or t.stride(0) * t.element_size() % 16 == 0)
+        t.shape[0] <= 1 or t.stride(0) * t.element_size() % 16 == 0 and t.stride(0) <= most)
     return t if taken else t.clone(memory_format=torch.contiguous_format)
 
 
@@ -252,6 +252,9 @@ def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor
 # gated scan
 # ---------------------------------------------------------------------------
 
+_MAX_SCAN_ROW_STRIDE = 1 << 21  # SSC_MAX_SCAN_ROW_STRIDE
+
+
 def _scan_shape(x, gate, offsets, h0, reverse, form):
     code = _dtype_code("ssc_gated_scan", x.dtype)
     if form not in SCAN_FORMS:
@@ -317,7 +320,7 @@ class GatedScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, gate, offsets, h0, reverse, form):
-        x, gate, h0 = _dense_rows(x), _dense_rows(gate), _packed(h0)
+        x, gate, h0 = _dense_rows(x, _MAX_SCAN_ROW_STRIDE), _dense_rows(gate, _MAX_SCAN_ROW_STRIDE), _packed(h0)
         y, last, carries = gated_scan_fwd(x, gate, offsets, h0, reverse, form, need_carries=any(ctx.needs_input_grad))
         ctx.save_for_backward(x, gate, offsets, h0, carries)
         ctx.rest = (reverse, form)
