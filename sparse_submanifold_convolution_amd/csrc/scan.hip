@@ -19,8 +19,8 @@
 // (4.6 TB/s); narrow ones by the exchange between tiles (800k rows x 64 channels: 0.11 and 0.18 ms, 2.8 TB/s).  In three
 // launches, with the inputs read twice and the tiles joined in between, the forward pass would move 5 tensors, not 3.
 //
-// A sample's first row has A = 0, and A = 0 drops whatever came before it, so samples never touch each other, not even
-// through an infinity or a NaN.  States, products and sums are fp32.  The backward pass forms h again from the inputs and
+// A sample's first row drops whatever came before it (A = -0, which no product of decays is), so samples never touch each
+// other, not even through an infinity or a NaN.  States, products and sums are fp32.  The backward pass forms h again from the inputs and
 // the values at the tiles' borders, which the forward pass hands out: y is not read and its rounding does not matter.
 
 #include <hip/hip_runtime.h>
@@ -134,9 +134,12 @@ struct Lane {
 // a value every lane holds alike, in a scalar register
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// The map (A, B) of a value, and its factor after an earlier map's: A = 0 drops what came before, a NaN among it too
-__device__ __forceinline__ float after(float A, float B, float v) { return A == 0.f ? B : fmaf(A, v, B); }
-__device__ __forceinline__ float times(float A, float a) { return A == 0.f ? 0.f : A * a; }
+// The map (A, B) of a value, and its factor after an earlier map's.  A = -0 drops what came before, a NaN among it too; a
+// product of decays that underflows is +0 and still hands on a NaN.
+constexpr float kDrop = -0.f;
+__device__ __forceinline__ bool drops(float A) { return __float_as_uint(A) == 0x80000000u; }
+__device__ __forceinline__ float after(float A, float B, float v) { return drops(A) ? B : fmaf(A, v, B); }
+__device__ __forceinline__ float times(float A, float a) { return drops(A) ? A : A * a; }
 
 // four elements of a row
 template <typename T>
@@ -297,7 +300,7 @@ __device__ __forceinline__ void give_word(uint64_t* at, float A, float B) {
 // kBunch.  Per channel, a lane of the first wave publishes the tile's map and composes those of the bunch's tiles before
 // it, and the last tile's publishes the bunch's; a lane of the second wave composes the maps of the kBunches bunches
 // before this one upon the value that reached the first of them, and the first tile's publishes the value that reaches the
-// bunch.  A value is a word with A = 0.
+// bunch.  A value is a word whose A hands nothing on.
 template <int CL, bool BACK>
 __device__ __forceinline__ void look_back(const ScanParams& p, int order, int group, const float (*tot)[2][4 * CL],
                                           float (*link)[2][4 * CL], float (&v)[4]) {
@@ -426,12 +429,13 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_fwd(ScanPara
         if (what != kNone && p.h0 && mine) load_state(p.h0 + int64_t(what >> 2) * p.c + c0, h);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          b[i][v] = what == kNone ? 0.f : (p.h0 ? fmaf(a[i][v], h[v], b[i][v]) : b[i][v]);
-          a[i][v] = A[v] = B[v] = 0.f;
+          b[i][v] = what == kNone ? 0.f : fmaf(a[i][v], h[v], b[i][v]);
+          a[i][v] = B[v] = 0.f;
+          A[v] = kDrop;
         }
       }
     }
-    // a NaN decay makes A one where it should stay 0, but B as well
+    // a NaN decay makes A one where it should stay -0, but B as well
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       B[v] = fmaf(a[i][v], B[v], b[i][v]);
@@ -555,10 +559,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanPara
       if (what & kLast) {  // kNone has all bits
         begin(p.dlast, what, Bb);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) Ab[v] = 0.f;
+        for (int v = 0; v < 4; ++v) Ab[v] = kDrop;
       }
     }
-    // a NaN decay makes A one where it should stay 0, but B as well
+    // a NaN decay makes A one where it should stay -0, but B as well
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       Bb[v] = a[i][v] * (dy[v] + Bb[v]);
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) scan_bwd(ScanPara
       if (what & kFirst) {
         begin(p.h0, what, B);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) A[v] = 0.f;
+        for (int v = 0; v < 4; ++v) A[v] = kDrop;
       }
     }
 #pragma unroll

@@ -147,6 +147,45 @@ def test_gates_at_the_ends(ssc):
     assert torch.isnan(y[2:, 3]).all() and not torch.isnan(y[:2]).any() and not torch.isnan(y[:, :3]).any()
 
 
+@pytest.mark.parametrize("form", ["mix", "sum"])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_a_nan_gate_of_the_first_row(ssc, form, reverse):
+    """With and without an initial state: a NaN decay times any state is NaN, in that channel and from that row on."""
+    x, gate, dy, off, h0, dl = (t.to(DEV) for t in _case(16, [300, 20], 64, "f32"))
+    first = 299 if reverse else 0
+    gate[first, 5] = float("nan")
+    for h in (None, h0):
+        y, last, c = ssc.gated_scan_fwd(x, gate, off, h, reverse, form, need_carries=True)
+        assert torch.isnan(y[:300, 5]).all() and torch.isnan(last[0, 5]) and torch.isnan(y).sum() == 300
+        dx, dg, _ = ssc.gated_scan_bwd(x, gate, c, dy, off, h, None, reverse, form)
+        # the gradient of a later row does not know of it, but every decay's gradient holds a state
+        assert torch.isnan(dg[:300, 5]).all() and torch.isnan(dg).sum() == 300
+        assert torch.isnan(dx).sum() == (1 if form == "mix" else 0)
+
+
+def test_two_calls_at_once(ssc):
+    """Calls on two streams, each with its own exchange between tiles."""
+    cases = [[t.to(DEV) for t in _case(17 + i, [9000, 4000], 256, "bf16")] for i in range(2)]
+
+    def run(case):
+        x, gate, dy, off, h0, dl = case
+        y, last, c = ssc.gated_scan_fwd(x, gate, off, h0, need_carries=True)
+        return (y, last, *ssc.gated_scan_bwd(x, gate, c, dy, off, h0, dl))
+
+    want = [run(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+
+
 def test_strided_and_packed(ssc):
     g = torch.Generator().manual_seed(9)
     both = torch.randn(700, 3 * 64, generator=g).to(torch.float16).to(DEV)
