@@ -53,12 +53,14 @@ def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device,
         raise ValueError(f"{name}: expected {dtype} [{'n' if n is None else n}, heads, head_dim] on {device}, "
                          f"got {t.dtype} {tuple(shape)} on {t.device}")
     rows, heads, dim = shape
+    size = dtype.itemsize
+    if dim * size % 16 == 0 and t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return rows, heads, dim, heads * dim if rows > 1 else 0, dim if heads > 1 else 0
     rs, hs, es = t.stride()
     if rows <= 1:
         rs = 0  # a single row's stride is never used and may be anything
     if heads <= 1:
         hs = 0
-    size = dtype.itemsize
     if dim > 1 and es != 1 or rs * size % 16 or hs * size % 16 or t.data_ptr() % 16:
         raise ValueError(f"{name}: a head's elements must be contiguous and rows and heads 16-byte aligned, "
                          f"got strides {t.stride()}")

@@ -23,10 +23,13 @@ SCAN_FORMS = {"mix": 0, "sum": 1}
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: tuple | None = None) -> int:
     """The row stride of a [n, channels] view whose rows are 16-byte vectors."""
-    if t.dim() != 2 or t.dtype != dtype or t.device != device or (shape is not None and tuple(t.shape) != tuple(shape)):
+    have = t.shape
+    if len(have) != 2 or t.dtype != dtype or t.device != device or (shape is not None and have != shape):
         want = "[n, channels]" if shape is None else list(shape)
         raise ValueError(f"{name}: expected {dtype} {want} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, channels = t.shape
+    rows, channels = have
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:  # the calls refuse rows that are not 16-byte vectors
+        return channels if rows > 1 else 0
     row, one = t.stride()
     if rows <= 1:
         row = 0  # a single row's stride is never used and may be anything
