@@ -678,8 +678,8 @@ enum ssc_scan_form { SSC_SCAN_MIX = 0, SSC_SCAN_SUM = 1 };
 /* Sizes of a call (a host struct, read during the call). */
 typedef struct ssc_scan_shape {
   int64_t n;                             /* rows, at most SSC_MAX_SEQ_ROWS; a workgroup of 256 threads takes 128 rows of
-                                          * 256 bytes (256 of 128, 512 of 64 where the rows are no longer), with fewer
-                                          * than 2^32 threads in all */
+                                          * 64 channels (256 of 32 where rows have no more), with fewer than 2^32
+                                          * threads in all */
   int64_t x_row_stride, gate_row_stride; /* elements, multiples of 16 bytes, 0 .. SSC_MAX_SCAN_ROW_STRIDE */
   int32_t batch;                         /* samples, 1 .. SSC_MAX_ATTN_BATCH */
   int32_t channels;                      /* whole 16-byte vectors, at most SSC_MAX_SEQ_CHANNELS */

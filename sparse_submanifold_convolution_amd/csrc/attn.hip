@@ -69,15 +69,17 @@ int64_t busy_wgs(int64_t rows, int64_t cols, const ssc_attn_shape& a) {
 }
 
 // Splits of the forward and dQ passes.  Rows: two workgroups a CU fill the chip; a split is worth its share of the join
-// from four 16-bit tiles on, and from one fp32 tile, whose products take about eight times as long.  Few rows: as
-// many workgroups as fit at once by their LDS, a whole number of times the rows', each wave with two tiles or more.
+// from four 16-bit tiles on, and from one fp32 tile, whose products take about eight times as long; from four too where a
+// window leaves few of them (2000 fp32 rows of four heads of 64, in a graph: 28.2 us in splits of four, 28.8 of one and
+// 37 in no split; ragged 40 wide: 19.9, 25.3 and 20.2; 1500 of 128: 38.7, 55.6 and 74).  Few rows: as many workgroups as
+// fit at once by their LDS, a whole number of times the rows', each wave with two tiles or more.
 int row_split(bool few, int64_t wgs, int64_t kv_tiles, const ssc_attn_shape& a, const Window* w) {
   const int e = esize(a.dtype);
   // a window's few tiles of narrow 16-bit heads are over before a join would be (17 tiles: 13.4 us a call in one split,
   // 16.0 in two; 33 tiles in a graph: 16.3 and, in four, 11.9)
   if (few && w && e == 2 && a.head_dim <= 64 && kv_tiles < 24) return 1;
   if (few) return pick_split(wgs, a.head_dim <= 64 ? 2 * kCUs : kCUs, kv_tiles, 8);
-  return wgs >= kCUs ? 1 : pick_split(wgs, 2 * kCUs, kv_tiles, e == 4 ? 1 : 4);
+  return wgs >= kCUs ? 1 : pick_split(wgs, 2 * kCUs, kv_tiles, e == 4 && !w ? 1 : 4);
 }
 
 FwdPlan fwd_plan(const ssc_attn_shape& a, const Window* w = nullptr) {
@@ -104,9 +106,10 @@ BwdPlan bwd_plan(const ssc_attn_shape& a, const Window* w = nullptr) {
   b.q_split = row_split(b.q_few, busy_wgs(rows, qc, a), kv_tiles, a, w);
   // dK and dV of short encoder sequences: few column tiles over long streams, split into several rounds of workgroups
   // so that the last round's idle CUs and the samples' different lengths matter little (fp32, whose blocks are long:
-  // half as many rounds).
+  // half as many rounds).  A window's fp32 splits take four tiles, as in row_split (the sizes there: 24.8 us, 26.5 in
+  // splits of two; 38.5 and 39.3; 40.4 and 47.9).
   const int64_t wgs = busy_wgs(a.nk, kc, a), want = (a.dtype == SSC_F32 ? 4 : 8) * kCUs;
-  b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? 2 : 8);
+  b.k_split = wgs >= want ? 1 : pick_split(wgs, want, q_tiles, a.dtype == SSC_F32 ? (w ? 4 : 2) : 8);
   if (w && w->sinks > 0) {
     // the sinks' launch is of single waves over all of a sample's tokens: about eight of them a CU, each with one fp32
     // tile at least (ragged fp32 training, 838 tokens of three heads: 27 us with two)
