@@ -314,43 +314,57 @@ struct Segment {
   int32_t index;   // of the segment: 0 before the first sample, b + 1 for sample b
 };
 
-// Finds tile t of the concatenated segments, each holding ceil(len * mult / cols) tiles (most: of its first rows, and of
-// the samples' only); false past the last.  Each lane looks at one segment; all offsets are loaded side by side.
+// Finds tile t of the segments; false where there is none.  Segment s of rows b .. e - 1 owns the tiles from
+// floor(b mult / cols) + s up to the next segment's, which are enough for its rows (ceil(x - y) <= floor(x) - floor(y) + 1)
+// and number the tiles of a launch without a table of where a segment's begin; it leaves the last of them idle where one
+// less would do.  The segment is the last one whose first tile is not past t: each lane looks at one of 64 candidates, and
+// in the last round (the only one up to 62 samples) at all of its offsets side by side.  A walk over the samples, 64 at a
+// time, took a time that grew with them (windows of 17 keys, 4 heads of 64, bf16, forward: 16,384 samples of 16 rows
+// 23 ms, and now 0.87; 1,024 of 256 rows 251 us, and 154).
+// most: tiles of the samples' first `most` rows only, as many for each sample where that is fewer in all.
 __device__ __forceinline__ bool find_segment(const int32_t* off, int64_t n, const int32_t* other_off, int64_t other_n,
                                              int batch, int mult, int cols, int t, Segment* seg, int most = 0x7FFFFFFF) {
   const int lane = threadIdx.x & 63;
-  for (int base = 0; base < batch + 2; base += 64) {
-    const int s = base + lane;
+  const int per = int64_t(most) * batch < n ? (most + cols - 1) / cols : 0;
+  int at = 0, end = batch + 2;
+  if (per > 0) {
+    at = t / per + 1;
+    if (at > batch) return false;
+    end = at + 1;
+  }
+  for (int step = 0; step != 1;) {
+    step = (end - at + 63) / 64;
+    const int s = at + lane * step;
+    const bool in = s < end;
     const int lo = s < 1 ? 0 : (s - 1 < batch ? s - 1 : batch), hi = s < batch ? s : batch;
-    int64_t b = clamp_off(off, lo, n), e = clamp_off(off, hi, n);
-    const int64_t ob = clamp_off(other_off, lo, other_n), oe = clamp_off(other_off, hi, other_n);
-    if (s == 0) b = 0;
-    if (s == batch + 1) e = n;
-    if (e < b || s > batch + 1) e = b;
-    const int len = int(e - b), olen = s >= 1 && s <= batch && oe > ob ? int(oe - ob) : 0;
-    const int head = most == 0x7FFFFFFF ? len : (s < 1 || s > batch ? 0 : (len < most ? len : most));
-    const int mine = int((int64_t(head) * mult + cols - 1) / cols);
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(incl, d);
-      if (lane >= d) incl += o;
+    int64_t b = clamp_off(off, lo, n), e = 0, ob = 0, oe = 0;
+    if (step == 1) {
+      e = clamp_off(off, hi, n);
+      ob = clamp_off(other_off, lo, other_n);
+      oe = clamp_off(other_off, hi, other_n);
     }
-    const int total = uniform(__shfl(incl, 63));
-    if (t < total) {
-      const int w = uniform(__ffsll((unsigned long long)__ballot(incl > t)) - 1);
+    if (s == 0) b = 0;
+    const int first = per > 0 ? (s - 1) * per : int(b * mult / cols) + s;
+    const int k = __popcll(__ballot(in && first <= t)) - 1, w = uniform(k < 0 ? 0 : k);
+    if (step == 1) {
+      if (s == batch + 1) e = n;
+      if (e < b) e = b;
+      const int len = int(e - b), olen = s >= 1 && s <= batch && oe > ob ? int(oe - ob) : 0;
       // rows are below 2^28: offsets fit an int
       seg->begin = __builtin_amdgcn_readlane(int(b), w);
       seg->len = __builtin_amdgcn_readlane(len, w);
-      seg->tile = t - __builtin_amdgcn_readlane(incl - mine, w);
+      seg->tile = t - __builtin_amdgcn_readlane(first, w);
       seg->other = __builtin_amdgcn_readlane(int(ob), w);
       seg->other_len = __builtin_amdgcn_readlane(olen, w);
-      seg->index = base + w;
-      return true;
+      seg->index = uniform(at) + w;
+    } else {
+      at += w * step;
+      end = at + step < end ? at + step : end;
     }
-    t -= total;
   }
-  return false;
+  if (most != 0x7FFFFFFF && (seg->index < 1 || seg->index > batch)) return false;
+  const int rows = seg->len < most ? seg->len : most;
+  return seg->tile >= 0 && int64_t(seg->tile) * cols < int64_t(rows) * mult;
 }
 
 __device__ __forceinline__ uint32_t div_g(uint32_t r, const Params& p) {

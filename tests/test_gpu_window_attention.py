@@ -116,6 +116,27 @@ def test_parity(ssc, case, dt):
     _check(ssc, _inputs(1, ql, kl, hq, hk, d, dt, masked), window)
 
 
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("batch", [62, 63, 64, 200, 4500])
+def test_many_samples(ssc, dt, batch):
+    """Samples past what one look at the offsets holds, some empty, and sinks that take fewer rows than there are or more."""
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 7, batch).tolist()
+    keys = rng.integers(0, 9, batch).tolist()
+    lens[batch // 2], keys[batch // 2] = 150, 150
+    for ql, kl, window in ((lens, lens, (1, 1, 1)), (lens, keys, (0, 2, 3)), ([1] * batch, keys, (3, 0, 40))):
+        print(f"[window] {dt} {batch} samples {window}", flush=True)
+        case = _inputs(14, ql, kl, 2, 1, 32, dt)
+        _check(ssc, case, window)
+        q, k, v, do, qo, ko, _ = (None if t is None else t.to(DEV) for t in case)
+        a, al = ssc.window_attention_fwd(q, k, v, qo, ko, None, None)
+        b, bl = ssc.cross_attention_fwd(q, k, v, qo, ko)
+        assert torch.equal(a, b) and torch.equal(al, bl)
+        for x, y in zip(ssc.window_attention_bwd(q, k, v, a, al, do, qo, ko, None, None),
+                        ssc.cross_attention_bwd(q, k, v, b, bl, do, qo, ko)):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("left", [0, 1, 31, 32, 33, 63, 64, 127, 128, 129])
 def test_edges_of_tiles(ssc, dt, left):
